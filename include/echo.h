@@ -53,7 +53,8 @@ enum {
   ECHO_ERR_STAGING = 7,        /* device: a request's prefetch cap exceeds its staging  */
   ECHO_ERR_SCRATCH_LIMIT = 8,  /* host: the call needs more than the library's built-in
                                   scratch (echo_sparse_mla_decode_noalloc only)         */
-  ECHO_ERR_NOT_RESIDENT = 9    /* device: a token to attend over has no GPU slot        */
+  ECHO_ERR_NOT_RESIDENT = 9,   /* device: a token to attend over has no GPU slot        */
+  ECHO_ERR_PAGE = 10           /* device: a needed page-table entry is not a page       */
 };
 
 enum { ECHO_F32 = 0, ECHO_BF16 = 1, ECHO_E4M3 = 2 };
@@ -602,6 +603,122 @@ echo_status_t echo_block_scores(const float *scores, const int32_t *seq_len, int
  */
 echo_status_t echo_expand_block_slots(const int32_t *sel_blk, const int32_t *block_slot, const int32_t *seq_len,
                                       int32_t B, int32_t kb, int32_t T, int32_t *out, echo_stream_t stream);
+
+/*
+ * Paged key/value cache, attended in full: the dense layers that stand beside the sparse
+ * ones, and GQA layers whose contexts stay on the GPU.  The pages have no counterpart on
+ * the review page; they follow this library's conventions (counts in device memory,
+ * sticky status instead of traps, no allocation, capturable in a CUDA Graph).
+ *
+ * Value e of KV head h of row i of page p lies at p*page_stride + i*row_stride +
+ * h*head_stride + e of k (keys) and of v (values), strides in values.  Token t of
+ * sequence b is row t % page_tokens of page page_table[b, t / page_tokens].
+ *   - head_dim is 64 or 128, dtype ECHO_BF16 or ECHO_F32, page_tokens any positive number;
+ *     k, v and every stride are multiples of 16 bytes.
+ *   - seq_len[b] (device) counts sequence b's tokens with the new ones of the call; it is
+ *     cut to [0, max_pages * page_tokens] (and INVALID_ARG set when it was not inside).
+ *   - q_start [B+1] (device, q_start[0] = 0, not descending): sequence b's new tokens are
+ *     rows q_start[b] .. q_start[b+1]-1 of the packed arrays; row i of n_b sits at position
+ *     seq_len[b] - n_b + i.  Rows from q_start[B] on are left as they were.  Entries are
+ *     cut to [0, N]; sequences that would overlap are the caller's error.
+ *   - Only page-table entries of tokens that a call writes, or that some row of it sees,
+ *     are used.  One outside [0, n_pages) sets ECHO_ERR_PAGE and its tokens are skipped.
+ *     Rows of the pages that hold no token of the sequence (at or past seq_len) may hold
+ *     anything, NaN too; keys and values below seq_len that some row of the call sees must
+ *     be finite (one that one row sees may reach another row's result as 0 * NaN).
+ *   - status: optional device int32, sticky (first error wins), zeroed by the caller.
+ */
+typedef struct {
+  void *k, *v;
+  int64_t page_stride, row_stride, head_stride;
+  int32_t n_pages, page_tokens, n_kv_heads, head_dim, dtype;
+  int32_t max_pages;          /* entries of one sequence's page-table row                 */
+  const int32_t *page_table;  /* [B, max_pages]                                           */
+  int32_t *status;            /* or NULL                                                  */
+} echo_paged_kv_t;
+
+/*
+ * Scores of paged attention, for a query at position p and a token t:
+ *   x = scale * q . key_t;  x = softcap * tanh(x / softcap) if softcap > 0;
+ *   x = x - slopes[head] * |p - t| if slopes is given.
+ * t is seen iff  first_tok <= t < seq_len  and
+ *   ((t <= p and (window == 0 or t > p - window)) or t < prefix_len).
+ */
+typedef struct {
+  float scale;
+  float softcap;              /* 0: none                                                  */
+  const float *slopes;        /* [Hq] or NULL                                             */
+  int32_t window;             /* 0: none                                                  */
+  const int32_t *first_tok;   /* [N] per row (decode: [B]) first token seen (its document's
+                                 start), or NULL: 0                                       */
+  const int32_t *prefix_len;  /* [B] tokens seen by every row of the sequence, before it or
+                                 after it (a two-way prefix, or first tokens kept outside a
+                                 window), or NULL: 0                                      */
+} echo_attn_scores_t;
+
+/* sizeof of echo_paged_kv_t and echo_attn_scores_t (see echo_abi_struct_sizes). */
+void echo_paged_struct_sizes(size_t out[2]);
+
+/*
+ * Append new tokens to a paged cache, with the rotation of their positions applied on the
+ * way.  For row n of sequence b at position p: the key heads of k [N, Hkv, d] (rotated)
+ * and the value heads of v [N, Hkv, d] are written to token p's page row; the query heads
+ * of q [N, Hq, d] (rotated) are written to q_out [N, Hq, d].
+ * The rotation turns pairs of the first rot_dim values of a head, pair j by cos_sin[p, j]
+ * and cos_sin[p, rot_dim/2 + j] (float32, [max_pos, rot_dim]): a' = a cos - b sin,
+ * b' = b cos + a sin, with (a, b) = values (j, j + rot_dim/2), or (2j, 2j + 1) if
+ * interleaved.  The other values are copied.  Arithmetic is float32, rounded once.
+ *   q, k, v rows may be strided (q_stride, k_stride, v_stride values from one row to the
+ *   next; the heads of a row are contiguous): slices of one fused projection.  q and
+ *   q_out may both be NULL (keys and values alone; Hq = 0).  q_out is contiguous; it may be
+ *   q itself when q is contiguous.
+ *   q_start: NULL means one new token for each sequence (N = B, row b is sequence b's).
+ *   rot_dim: 0 (no rotation, cos_sin NULL) or a multiple of 16 up to d.
+ * Device errors: PAGE (the row's key and value are not written); INVALID_ARG if a position
+ * lies outside [0, max_pages * page_tokens), or outside [0, max_pos) with a rotation (the
+ * row is skipped, q_out too).
+ */
+echo_status_t echo_paged_append(const echo_paged_kv_t *cache, const void *q, int64_t q_stride, const void *k,
+                                int64_t k_stride, const void *v, int64_t v_stride, void *q_out,
+                                const int32_t *q_start, const int32_t *seq_len, int32_t N, int32_t B, int32_t Hq,
+                                const float *cos_sin, int32_t max_pos, int32_t rot_dim, int32_t interleaved,
+                                echo_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over a paged cache (grouped query heads: head i
+ * reads KV head i / (Hq / n_kv_heads)).  The query of sequence b sits at seq_len[b] - 1.
+ *   out[b,i,:] = sum_t softmax_t(x) value_t;  lse[b,i] = log sum_t exp(x)   over seen t
+ *   q [B, Hq, d] (q_stride values from row to row); out [B, Hq, d] contiguous, the cache's
+ *   dtype; lse [B, Hq] float32; Hq / n_kv_heads a whole number up to 128.
+ *   workspace: echo_paged_decode_workspace_bytes(Hq, n_kv_heads, d) bytes, whatever the
+ *   batch and the lengths; nothing in it has to be set or is kept between calls; calls
+ *   that may overlap on the GPU need workspaces of their own.
+ * The cache's tiles are dealt out evenly over the GPU from the lengths found on the
+ * device, so one captured graph serves growing and ragged lengths.
+ * A row that sees no token gives out = 0 and lse = -inf.  Device errors: PAGE, INVALID_ARG.
+ */
+size_t echo_paged_decode_workspace_bytes(int32_t Hq, int32_t n_kv_heads, int32_t d);
+echo_status_t echo_paged_attn_decode(const echo_paged_kv_t *cache, const void *q, int64_t q_stride,
+                                     const int32_t *seq_len, int32_t B, int32_t Hq, const echo_attn_scores_t *scores,
+                                     void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                     echo_stream_t stream);
+
+/*
+ * Attention of many new tokens over a paged cache: prompts, chunks of prompts, a few
+ * drafted tokens per sequence (append them first).  As echo_paged_attn_decode for each
+ * packed row of q [N, Hq, d]; out [N, Hq, d] and lse [N, Hq] rows from q_start[B] on are
+ * left as they were.
+ *   workspace: echo_paged_prefill_workspace_bytes(N, B, Hq, n_kv_heads, d) bytes (0 when
+ *   the call needs none), as for echo_paged_attn_decode.
+ * Device errors: PAGE; INVALID_ARG (seq_len outside its range or shorter than the
+ * sequence's new rows, whose rows at negative positions see nothing); TIMEOUT if a bounded
+ * wait gave up (the call's results are not valid).
+ */
+size_t echo_paged_prefill_workspace_bytes(int32_t N, int32_t B, int32_t Hq, int32_t n_kv_heads, int32_t d);
+echo_status_t echo_paged_attn_prefill(const echo_paged_kv_t *cache, const void *q, int64_t q_stride,
+                                      const int32_t *q_start, const int32_t *seq_len, int32_t N, int32_t B,
+                                      int32_t Hq, const echo_attn_scores_t *scores, void *out, float *lse,
+                                      void *workspace, size_t workspace_bytes, echo_stream_t stream);
 
 #ifdef __cplusplus
 }

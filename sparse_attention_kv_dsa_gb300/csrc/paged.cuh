@@ -1,0 +1,110 @@
+// Shared parts of the paged-cache calls: argument checks, page-table look-ups, the range
+// of tokens that a query sees, and the base-2 form of its scores.
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+
+namespace echo {
+
+constexpr float kPgLog2e = 1.4426950408889634f;
+constexpr float kPgLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------------ host checks --
+inline int paged_elem_size(int dtype) { return dtype == ECHO_F32 ? 4 : 2; }
+
+inline echo_status_t paged_check(const echo_paged_kv_t *c) {
+  if (!c || !c->k || !c->v || !c->page_table || c->n_pages <= 0 || c->page_tokens <= 0 || c->n_kv_heads <= 0 ||
+      c->max_pages <= 0)
+    return ECHO_ERR_INVALID_ARG;
+  if ((c->head_dim != 64 && c->head_dim != 128) || (c->dtype != ECHO_BF16 && c->dtype != ECHO_F32))
+    return ECHO_ERR_UNSUPPORTED;
+  // positions, and positions rounded up to a tile, stay below 2^31
+  if ((int64_t)c->max_pages * c->page_tokens > 0x7fff0000ll) return ECHO_ERR_UNSUPPORTED;
+  const int64_t es = paged_elem_size(c->dtype);
+  if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15) return ECHO_ERR_INVALID_ARG;
+  if ((c->page_stride * es | c->row_stride * es | c->head_stride * es) & 15) return ECHO_ERR_INVALID_ARG;
+  return ECHO_OK;
+}
+
+inline echo_status_t paged_scores_check(const echo_attn_scores_t *s) {
+  if (!s || !std::isfinite(s->scale) || !std::isfinite(s->softcap) || s->softcap < 0.f || s->window < 0)
+    return ECHO_ERR_INVALID_ARG;
+  return ECHO_OK;
+}
+
+// Rows of packed heads: 16-byte aligned, a whole number of 16-byte chunks apart.
+inline bool paged_rows_ok(const void *p, int64_t stride, int dtype) {
+  return !((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * paged_elem_size(dtype))) & 15);
+}
+
+// ----------------------------------------------------------------- device parts --
+__device__ __forceinline__ void paged_fail(int32_t *status, int32_t code) {
+  if (status) atomicCAS(status, 0, code);
+}
+
+// Tokens of sequence b, cut to what its page-table row can hold.
+__device__ __forceinline__ int paged_len(const echo_paged_kv_t &C, const int32_t *seq_len, int b) {
+  const int cap = C.max_pages * C.page_tokens;
+  const int n = seq_len[b];
+  if (n < 0 || n > cap) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
+  return min(max(n, 0), cap);
+}
+
+// Offset (in values) of head 0 of token t's row, or -1 when its page-table entry is not a page.
+__device__ __forceinline__ int64_t paged_row(const echo_paged_kv_t &C, int b, int t) {
+  const int pg = t / C.page_tokens;
+  const int32_t e = __ldg(C.page_table + (int64_t)b * C.max_pages + pg);
+  if (e < 0 || e >= C.n_pages) {
+    paged_fail(C.status, ECHO_ERR_PAGE);
+    return -1;
+  }
+  return (int64_t)e * C.page_stride + (int64_t)(t - pg * C.page_tokens) * C.row_stride;
+}
+
+// Scores in base-2 units: log2(e) * x of a raw product s = q . k.
+//   no cap:  s * a                    with a = scale log2(e)
+//   cap:     c tanh(s a)              with a = scale / cap, c = cap log2(e)
+// tanh(y) = 1 - 2 / (2^(2 y log2 e) + 1): its error stays near 1e-7 (absolute), so a score
+// is off by about 1e-7 of the cap, where the approximate tanh instruction is off by 5e-4.
+struct ScoreForm {
+  float a, c;
+  int capped;
+};
+inline ScoreForm score_form(const echo_attn_scores_t *s) {
+  ScoreForm f;
+  f.capped = s->softcap > 0.f;
+  f.a = f.capped ? (float)(2.0 * 1.4426950408889634 * (double)s->scale / (double)s->softcap) : s->scale * kPgLog2e;
+  f.c = s->softcap * kPgLog2e;
+  return f;
+}
+__device__ __forceinline__ float score_log2(const ScoreForm &f, float s) {
+  const float y = s * f.a;
+  return f.capped ? f.c * (1.f - __fdividef(2.f, exp2f(y) + 1.f)) : y;
+}
+
+// The tiles of `tile` tokens that hold [first, pre) or [lo, hi): tiles tA .. tA + nA - 1, then
+// tB .. tB + nB - 1, in ascending order and without a tile twice.
+struct TileSpan {
+  int tA, nA, tB, nB;
+  __device__ __forceinline__ int tile(int i) const { return i < nA ? tA + i : tB + (i - nA); }
+};
+__device__ __forceinline__ TileSpan tile_span(int first, int pre, int lo, int hi, int tile) {
+  TileSpan s = {0, 0, 0, 0};
+  int eA = 0, eB = 0;
+  const bool a = first < pre, b = lo < hi;
+  if (a) { s.tA = first / tile; eA = (pre + tile - 1) / tile; }
+  if (b) { s.tB = lo / tile; eB = (hi + tile - 1) / tile; }
+  if (a && b && s.tB <= eA) {                    // they touch: one run (lo >= first)
+    s.tA = min(s.tA, s.tB);
+    eA = max(eA, eB);
+  } else if (b) {
+    s.nB = eB - s.tB;
+  }
+  s.nA = a ? eA - s.tA : 0;
+  return s;
+}
+
+}  // namespace echo

@@ -18,6 +18,7 @@ from . import build as _build
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_POOL_EXHAUSTED, ERR_HOST_INDEX, ERR_STAGING = range(8)
 ERR_SCRATCH_LIMIT = 8
 ERR_NOT_RESIDENT = 9
+ERR_PAGE = 10
 MLA_NOALLOC_SCRATCH_BYTES = 32 << 20
 PF_DEFER_CAP = 1            # echo_index_prefetch flag: exact cap restored by echo_topk_prefetch
 F32, BF16, E4M3 = 0, 1, 2
@@ -29,7 +30,8 @@ PENDING_LIST_MIN_SLOTS = 14080  # ECHO_PENDING_LIST_MIN_SLOTS: pools that keep t
 
 STATUS_NAMES = {OK: "OK", ERR_INVALID_ARG: "INVALID_ARG", ERR_UNSUPPORTED: "UNSUPPORTED", ERR_CUDA: "CUDA",
                 ERR_TIMEOUT: "TIMEOUT", ERR_POOL_EXHAUSTED: "POOL_EXHAUSTED", ERR_HOST_INDEX: "HOST_INDEX",
-                ERR_STAGING: "STAGING", ERR_SCRATCH_LIMIT: "SCRATCH_LIMIT", ERR_NOT_RESIDENT: "NOT_RESIDENT"}
+                ERR_STAGING: "STAGING", ERR_SCRATCH_LIMIT: "SCRATCH_LIMIT", ERR_NOT_RESIDENT: "NOT_RESIDENT",
+                ERR_PAGE: "PAGE"}
 
 
 class EchoError(RuntimeError):
@@ -72,6 +74,19 @@ class HostPoolT(ctypes.Structure):
                 ("free_rows", ctypes.c_int64 * HOST_POOL_MAX_RANGES)]
 
 
+class PagedKVT(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
+class AttnScoresT(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int32), ("first_tok", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p)]
+
+
 # Declared signatures: name -> (restype, argtypes).  P = pointer, I = int32.
 _P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 SIGNATURES = {
@@ -106,6 +121,13 @@ SIGNATURES = {
     "echo_host_pool_alloc": (_I, [_P, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
     "echo_host_pool_free": (_I, [_P, ctypes.c_int64, ctypes.c_int64]),
     "echo_host_pool_layer": (_I, [_P, _I, ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p)]),
+    "echo_paged_struct_sizes": (None, [_P]),
+    "echo_paged_append": (_I, [_P, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, _I, _I, _I,
+                               _P, _I, _I, _I, _P]),
+    "echo_paged_decode_workspace_bytes": (_S, [_I, _I, _I]),
+    "echo_paged_attn_decode": (_I, [_P, _P, ctypes.c_int64, _P, _I, _I, _P, _P, _P, _P, _S, _P]),
+    "echo_paged_prefill_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "echo_paged_attn_prefill": (_I, [_P, _P, ctypes.c_int64, _P, _P, _I, _I, _I, _P, _P, _P, _P, _S, _P]),
     "echo_cache_status": (_I, [_P, ctypes.POINTER(ctypes.c_int32)]),
     "echo_cache_read_counters": (_I, [_P, ctypes.POINTER(ctypes.c_int32)]),
 }
@@ -414,3 +436,165 @@ def expand_block_slots(sel_blk, block_slot, seq_len, T: int, out, stream=None):
     B, kb = sel_blk.shape
     check(lib().echo_expand_block_slots(ptr(sel_blk), ptr(block_slot), ptr(seq_len), B, kb, int(T), ptr(out),
                                         stream_handle(stream)), "expand_block_slots")
+
+
+# ------------------------------------------------------------- paged KV cache --
+def _bad(where: str, what: str):
+    raise EchoError(ERR_INVALID_ARG, f"{where} ({what})")
+
+
+def _i32(t, shape, dev, where: str, name: str):
+    """A contiguous int32 tensor of this shape on this device, or None."""
+    if t is not None and (t.dtype is not torch.int32 or t.shape != shape or t.device != dev or not t.is_contiguous()):
+        _bad(where, f"{name}: contiguous int32 {list(shape)} on {dev}")
+    return ptr(t)
+
+
+def _paged(k_pages, v_pages, page_table, seq_len, status, where: str):
+    """echo_paged_kv_t of k_pages and v_pages [n_pages, page_tokens, Hkv, d]: any strides with
+    a unit last one, the same for both (pages laid out heads first are a transposed view)."""
+    dev = k_pages.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        _bad(where, "k_pages: on the current CUDA device")
+    shape = k_pages.shape
+    if (len(shape) != 4 or v_pages.shape != shape or k_pages.dtype is not v_pages.dtype or v_pages.device != dev
+            or 0 in shape):
+        _bad(where, "k_pages, v_pages: [n_pages, page_tokens, Hkv, d] of one shape, type and device")
+    if k_pages.dtype is torch.bfloat16:
+        dt = BF16
+    elif k_pages.dtype is torch.float32:
+        dt = F32
+    else:
+        raise EchoError(ERR_UNSUPPORTED, f"{where} (bfloat16 or float32)")
+    ks = [s if n > 1 else 0 for s, n in zip(k_pages.stride(), shape)]
+    if ks != [s if n > 1 else 0 for s, n in zip(v_pages.stride(), shape)] or (ks[3] != 1 and shape[3] > 1):
+        _bad(where, "k_pages, v_pages: the same strides, the last one 1")
+    if page_table.dim() != 2 or 0 in page_table.shape or seq_len.dim() != 1 or seq_len.shape[0] != page_table.shape[0]:
+        _bad(where, "page_table: [B, max_pages], seq_len: [B]")
+    return PagedKVT(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], shape[0], shape[1], shape[2],
+                    shape[3], dt, page_table.shape[1], _i32(page_table, page_table.shape, dev, where, "page_table"),
+                    _i32(status, (1,), dev, where, "status"))
+
+
+def _head_rows(t, N: int, d: int, pages, where: str, name: str) -> int:
+    """Row stride of packed heads t [N, H, d]: a row's heads are contiguous, rows may be strided."""
+    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != d or t.dtype is not pages.dtype or t.device != pages.device:
+        _bad(where, f"{name}: [{N}, H, {d}], the cache's type and device")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != d and t.shape[1] > 1):
+        _bad(where, f"{name}: the heads of a row contiguous")
+    return s[0] if N > 1 else t.shape[1] * d
+
+
+def _attn_scores(scale, softcap, window, slopes, first_tok, prefix_len, rows: int, B: int, Hq: int, dev, where: str):
+    if slopes is not None and (slopes.dtype is not torch.float32 or slopes.shape != (Hq,) or slopes.device != dev
+                               or not slopes.is_contiguous()):
+        _bad(where, f"slopes: contiguous float32 [{Hq}] on {dev}")
+    return AttnScoresT(scale, softcap, ptr(slopes), window, _i32(first_tok, (rows,), dev, where, "first_tok"),
+                       _i32(prefix_len, (B,), dev, where, "prefix_len"))
+
+
+def _attn_buffers(q, out, lse, workspace, nbytes: int, stream, where: str):
+    """out, lse and the workspace: the caller's, or new ones."""
+    new = []
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        new.append(out)
+    elif out.shape != q.shape or out.dtype is not q.dtype or out.device != q.device or not out.is_contiguous():
+        _bad(where, f"out: contiguous, {list(q.shape)}, as q")
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        new.append(lse)
+    elif (lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or lse.device != q.device
+          or not lse.is_contiguous()):
+        _bad(where, f"lse: contiguous float32 {list(q.shape[:2])}")
+    if workspace is None:
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            new.append(workspace)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        _bad(where, "workspace: contiguous, on q's device")
+    if stream is not None:
+        for t in new:
+            t.record_stream(stream)
+    return out, lse, workspace
+
+
+def paged_append(k, v, k_pages, v_pages, page_table, seq_len, *, q=None, q_out=None, cos_sin=None,
+                 interleaved: bool = False, q_start=None, status=None, stream=None):
+    """Append k, v [N, Hkv, d] to the pages at the last positions of each sequence, keys rotated
+    by cos_sin [max_pos, rot_dim] (float32 cosines, then sines); q [N, Hq, d], rotated alike,
+    goes to q_out (allocated if not given), which is returned.  seq_len [B] counts the new
+    tokens; q_start [B + 1] gives each sequence's rows (None: one row each)."""
+    w = "paged_append"
+    c = _paged(k_pages, v_pages, page_table, seq_len, status, w)
+    dev, B, N, d = k_pages.device, page_table.shape[0], k.shape[0], c.head_dim
+    ks, vs = _head_rows(k, N, d, k_pages, w, "k"), _head_rows(v, N, d, k_pages, w, "v")
+    if k.shape[1] != c.n_kv_heads or v.shape[1] != c.n_kv_heads:
+        _bad(w, f"k, v: [N, {c.n_kv_heads}, {d}]")
+    Hq = qs = 0
+    if q is not None:
+        qs, Hq = _head_rows(q, N, d, k_pages, w, "q"), q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            if stream is not None:
+                q_out.record_stream(stream)
+        elif q_out.shape != q.shape or q_out.dtype is not q.dtype or q_out.device != dev or not q_out.is_contiguous():
+            _bad(w, "q_out: contiguous, as q")
+    elif q_out is not None:
+        _bad(w, "q_out without q")
+    rot = max_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype is not torch.float32 or cos_sin.device != dev or not cos_sin.is_contiguous():
+            _bad(w, "cos_sin: contiguous float32 [max_pos, rot_dim]")
+        max_pos, rot = cos_sin.shape
+    check(lib().echo_paged_append(ctypes.byref(c), ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, ptr(q_out),
+                                  _i32(q_start, (B + 1,), dev, w, "q_start"), _i32(seq_len, (B,), dev, w, "seq_len"),
+                                  N, B, Hq, ptr(cos_sin), max_pos, rot, interleaved, stream_handle(stream)), w)
+    return q_out
+
+
+def paged_decode_workspace_bytes(Hq: int, n_kv_heads: int, d: int) -> int:
+    return int(lib().echo_paged_decode_workspace_bytes(Hq, n_kv_heads, d))
+
+
+def paged_attn_decode(q, k_pages, v_pages, page_table, seq_len, scale: float, *, softcap: float = 0.0, window: int = 0,
+                      slopes=None, first_tok=None, prefix_len=None, out=None, lse=None, workspace=None, status=None,
+                      stream=None):
+    """Attention of one new token per sequence, q [B, Hq, d], over its pages -> (out, lse)."""
+    w = "paged_attn_decode"
+    c = _paged(k_pages, v_pages, page_table, seq_len, status, w)
+    B, Hq, dev, L = page_table.shape[0], q.shape[1], k_pages.device, lib()
+    qs = _head_rows(q, B, c.head_dim, k_pages, w, "q")
+    sc = _attn_scores(scale, softcap, window, slopes, first_tok, prefix_len, B, B, Hq, dev, w)
+    nbytes = L.echo_paged_decode_workspace_bytes(Hq, c.n_kv_heads, c.head_dim) if workspace is None else 0
+    out, lse, workspace = _attn_buffers(q, out, lse, workspace, nbytes, stream, w)
+    check(L.echo_paged_attn_decode(ctypes.byref(c), q.data_ptr(), qs, _i32(seq_len, (B,), dev, w, "seq_len"), B, Hq,
+                                   ctypes.byref(sc), out.data_ptr(), lse.data_ptr(), ptr(workspace),
+                                   workspace.nbytes if workspace is not None else 0, stream_handle(stream)), w)
+    return out, lse
+
+
+def paged_prefill_workspace_bytes(N: int, B: int, Hq: int, n_kv_heads: int, d: int) -> int:
+    return int(lib().echo_paged_prefill_workspace_bytes(N, B, Hq, n_kv_heads, d))
+
+
+def paged_attn_prefill(q, q_start, k_pages, v_pages, page_table, seq_len, scale: float, *, softcap: float = 0.0,
+                       window: int = 0, slopes=None, first_tok=None, prefix_len=None, out=None, lse=None,
+                       workspace=None, status=None, stream=None):
+    """Attention of the packed new tokens q [N, Hq, d] (rows q_start[b] .. q_start[b+1]-1 are
+    sequence b's last tokens) over their sequences' pages -> (out, lse)."""
+    w = "paged_attn_prefill"
+    c = _paged(k_pages, v_pages, page_table, seq_len, status, w)
+    N, B, Hq, dev, L = q.shape[0], page_table.shape[0], q.shape[1], k_pages.device, lib()
+    qs = _head_rows(q, N, c.head_dim, k_pages, w, "q")
+    if q_start is None:
+        _bad(w, "q_start: int32 [B + 1]")
+    sc = _attn_scores(scale, softcap, window, slopes, first_tok, prefix_len, N, B, Hq, dev, w)
+    nbytes = L.echo_paged_prefill_workspace_bytes(N, B, Hq, c.n_kv_heads, c.head_dim) if workspace is None else 0
+    out, lse, workspace = _attn_buffers(q, out, lse, workspace, nbytes, stream, w)
+    check(L.echo_paged_attn_prefill(ctypes.byref(c), q.data_ptr(), qs, _i32(q_start, (B + 1,), dev, w, "q_start"),
+                                    _i32(seq_len, (B,), dev, w, "seq_len"), N, B, Hq, ctypes.byref(sc),
+                                    out.data_ptr(), lse.data_ptr(), ptr(workspace),
+                                    workspace.nbytes if workspace is not None else 0, stream_handle(stream)), w)
+    return out, lse
