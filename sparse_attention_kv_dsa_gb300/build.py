@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libecho.so")
 SOURCES = ["cache.cu", "indexer.cu", "topk.cu", "mla.cu", "step.cu", "prefill.cu", "blocks.cu", "gqa.cu",
-           "paged_append.cu", "paged_decode.cu", "paged_prefill.cu", "hostpool.cpp"]
+           "paged_append.cu", "paged_decode.cu", "paged_prefill.cu", "paged_prefill_tc.cu", "hostpool.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

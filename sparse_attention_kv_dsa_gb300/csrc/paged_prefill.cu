@@ -5,39 +5,14 @@
 // token r / G, head r % G of the group, so that every tile of rows reads its keys and values
 // once whatever G is, and a few drafted tokens still fill a tile.
 //
-// CUDA-core kernel: one CTA takes 64 packed rows of one (sequence, KV head) and walks the
+// bf16 runs on the tensor cores (paged_prefill_tc.cu).  Float32 (below): one CTA takes 64 packed rows of one (sequence, KV head) and walks the
 // 64-token tiles that some row sees, with a running maximum and sum; 256 threads hold 4 x 4
 // scores and 4 x d/16 results each.  Float32 arithmetic throughout: 4 d operations for each
 // pair of query head and seen token on the FMA units.
 
-#include "paged.cuh"
+#include "paged_prefill.cuh"
 
 namespace echo {
-
-struct PrefillParams {
-  echo_paged_kv_t C;
-  const void *q;
-  int64_t q_stride;
-  const int32_t *q_start, *seq_len;
-  int N, B, Hq, G;
-  const float *slopes;
-  int window;
-  const int32_t *first_tok, *prefix_len;
-  ScoreForm f;
-  void *out;
-  float *lse;
-};
-
-// Rows of sequence b: [s0, s0 + n).
-struct SeqRows {
-  int s0, n;
-};
-__device__ __forceinline__ SeqRows seq_rows(const PrefillParams &P, int b) {
-  SeqRows r;
-  r.s0 = min(max(P.q_start[b], 0), P.N);
-  r.n = max(min(max(P.q_start[b + 1], 0), P.N) - r.s0, 0);
-  return r;
-}
 
 // The sequence and row tile of tile index x: the x-th tile of `rows` packed rows, sequences in
 // order; false past the last one.  Every thread of the block calls it (128 or more).
@@ -83,18 +58,9 @@ constexpr size_t ps_smem() {
   return sizeof(float) * ((size_t)PS_ROWS * D + (size_t)PS_KEYS * (D + 4) + (size_t)PS_ROWS * PS_PS);
 }
 
-template <typename T>
-__device__ __forceinline__ float4 ps_load4(const T *p) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float4 *>(p);
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-  }
-}
+__device__ __forceinline__ float4 ps_load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(PS_THREADS) paged_prefill_simt_kernel(const __grid_constant__ PrefillParams P) {
   extern __shared__ __align__(16) float ps_sm[];
   float *qs = ps_sm;                                     // [64][D]
@@ -139,7 +105,7 @@ __global__ void __launch_bounds__(PS_THREADS) paged_prefill_simt_kernel(const __
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < nr) {
       const int t = (r0 + r) / G, g = (r0 + r) % G;
-      v = ps_load4((const T *)P.q + (int64_t)(R.s0 + t) * P.q_stride + (int64_t)(kvh * G + g) * D + 4 * c);
+      v = ps_load4((const float *)P.q + (int64_t)(R.s0 + t) * P.q_stride + (int64_t)(kvh * G + g) * D + 4 * c);
     }
     *reinterpret_cast<float4 *>(qs + r * D + 4 * c) = v;
   }
@@ -156,7 +122,7 @@ __global__ void __launch_bounds__(PS_THREADS) paged_prefill_simt_kernel(const __
 #pragma unroll
     for (int j = 0; j < OC; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
   }
-  const T *kb = (const T *)P.C.k + (int64_t)kvh * P.C.head_stride, *vb = (const T *)P.C.v + (int64_t)kvh * P.C.head_stride;
+  const float *kb = (const float *)P.C.k + (int64_t)kvh * P.C.head_stride, *vb = (const float *)P.C.v + (int64_t)kvh * P.C.head_stride;
   const int nt = span.nA + span.nB;
   for (int it = 0; it < nt; ++it) {
     const int t0 = span.tile(it) * PS_KEYS;
@@ -258,29 +224,22 @@ __global__ void __launch_bounds__(PS_THREADS) paged_prefill_simt_kernel(const __
     const int t = (r0 + r) / G, g = (r0 + r) % G;
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     const int64_t row = (int64_t)(R.s0 + t) * P.Hq + kvh * G + g;
-    T *dst = (T *)P.out + row * D + 4 * tx;
+    float *dst = (float *)P.out + row * D + 4 * tx;
 #pragma unroll
-    for (int j = 0; j < OC; ++j) {
-      const float v[4] = {o[i][j][0] * inv, o[i][j][1] * inv, o[i][j][2] * inv, o[i][j][3] * inv};
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(dst + 64 * j) = make_float4(v[0], v[1], v[2], v[3]);
-      } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), c = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<__nv_bfloat162 *>(dst + 64 * j) = a;
-        *reinterpret_cast<__nv_bfloat162 *>(dst + 64 * j + 2) = c;
-      }
-    }
+    for (int j = 0; j < OC; ++j)
+      *reinterpret_cast<float4 *>(dst + 64 * j) =
+          make_float4(o[i][j][0] * inv, o[i][j][1] * inv, o[i][j][2] * inv, o[i][j][3] * inv);
     if (tx == 0) P.lse[row] = L == 0.f ? -INFINITY : (m[i] + log2f(L)) * kPgLn2;
   }
 }
 
-template <typename T, int D>
+template <int D>
 static echo_status_t launch_simt(const PrefillParams &P, cudaStream_t st) {
   const int64_t tiles = ((int64_t)P.N * P.G + PS_ROWS - 1) / PS_ROWS + P.B;
   if (tiles > 0x7fffffff) return ECHO_ERR_UNSUPPORTED;
-  ECHO_CUDA_OK(cudaFuncSetAttribute(paged_prefill_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  ECHO_CUDA_OK(cudaFuncSetAttribute(paged_prefill_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)ps_smem<D>()));
-  paged_prefill_simt_kernel<T, D><<<dim3((unsigned)tiles, P.C.n_kv_heads), PS_THREADS, ps_smem<D>(), st>>>(P);
+  paged_prefill_simt_kernel<D><<<dim3((unsigned)tiles, P.C.n_kv_heads), PS_THREADS, ps_smem<D>(), st>>>(P);
   ECHO_LAUNCH_OK();
   return ECHO_OK;
 }
@@ -289,9 +248,13 @@ static echo_status_t launch_simt(const PrefillParams &P, cudaStream_t st) {
 
 using namespace echo;
 
+// bf16: two partials a CTA, of the rows of a row tile at most, and a record each; float32: none
+// is needed, but the size does not ask for the type.
+static int prefill_prows(int64_t N, int64_t G) { return (int)std::min<int64_t>(PF_ROWS, N * G); }
+
 extern "C" size_t echo_paged_prefill_workspace_bytes(int32_t N, int32_t B, int32_t Hq, int32_t n_kv_heads, int32_t d) {
-  (void)N; (void)B; (void)Hq; (void)n_kv_heads; (void)d;
-  return 0;
+  if (N <= 0 || B <= 0 || Hq <= 0 || n_kv_heads <= 0 || d <= 0 || Hq % n_kv_heads) return 0;
+  return (size_t)PF_MAX_CTAS * (2 * (size_t)prefill_prows(N, Hq / n_kv_heads) * (d + 2) + 8) * sizeof(float);
 }
 
 extern "C" echo_status_t echo_paged_attn_prefill(const echo_paged_kv_t *cache, const void *q, int64_t q_stride,
@@ -302,10 +265,12 @@ extern "C" echo_status_t echo_paged_attn_prefill(const echo_paged_kv_t *cache, c
   if (st == ECHO_OK) st = paged_scores_check(scores);
   if (st != ECHO_OK) return st;
   if (!q || !q_start || !seq_len || !out || !lse || N <= 0 || B <= 0 || Hq <= 0) return ECHO_ERR_INVALID_ARG;
-  if (Hq % cache->n_kv_heads || Hq / cache->n_kv_heads > 128 || cache->n_kv_heads > 65535) return ECHO_ERR_UNSUPPORTED;
+  if (Hq % cache->n_kv_heads || Hq / cache->n_kv_heads > 128 || cache->n_kv_heads > 65535 || B > PF_MAX_B)
+    return ECHO_ERR_UNSUPPORTED;
   if (!paged_rows_ok(q, q_stride, cache->dtype) || !paged_rows_ok(out, 0, cache->dtype)) return ECHO_ERR_INVALID_ARG;
-  const size_t need = echo_paged_prefill_workspace_bytes(N, B, Hq, cache->n_kv_heads, cache->head_dim);
-  if (need && (!workspace || workspace_bytes < need)) return ECHO_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) ||
+      workspace_bytes < echo_paged_prefill_workspace_bytes(N, B, Hq, cache->n_kv_heads, cache->head_dim))
+    return ECHO_ERR_INVALID_ARG;
   PrefillParams P;
   P.C = *cache;
   P.q = q; P.q_stride = q_stride; P.q_start = q_start; P.seq_len = seq_len;
@@ -316,7 +281,12 @@ extern "C" echo_status_t echo_paged_attn_prefill(const echo_paged_kv_t *cache, c
   P.f = score_form(scores);
   P.out = out; P.lse = lse;
   cudaStream_t cs = (cudaStream_t)stream;
-  if (cache->dtype == ECHO_BF16)
-    return cache->head_dim == 128 ? launch_simt<__nv_bfloat16, 128>(P, cs) : launch_simt<__nv_bfloat16, 64>(P, cs);
-  return cache->head_dim == 128 ? launch_simt<float, 128>(P, cs) : launch_simt<float, 64>(P, cs);
+  if (cache->dtype == ECHO_BF16) {
+    P.prows = prefill_prows(N, P.G);
+    P.po = reinterpret_cast<float *>(workspace);
+    P.pml = P.po + (size_t)2 * PF_MAX_CTAS * P.prows * cache->head_dim;
+    P.rec = reinterpret_cast<int32_t *>(P.pml + (size_t)2 * PF_MAX_CTAS * P.prows * 2);
+    return launch_prefill_tc(P, cs);
+  }
+  return cache->head_dim == 128 ? launch_simt<128>(P, cs) : launch_simt<64>(P, cs);
 }

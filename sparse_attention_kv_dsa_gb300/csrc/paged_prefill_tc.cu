@@ -1,0 +1,760 @@
+// Tensor-core form (bf16) of the many-token attention over a paged key/value cache.
+//
+// Bound: 4 d operations for each pair of query head and seen token on the tensor cores, and
+// one power (with a cap: a tanh too) on the special-function units.
+//
+// A persistent CTA per SM.  The work is dealt out in units -- one 128-token tile of the cache
+// for one row tile of 256 packed rows (token r / G, head r % G of the KV head's group) --
+// ordered by (sequence, row tile, KV head, tile); every CTA takes an equal run of them, found
+// from the device's own lengths and masks, so that ragged prompts, the triangle of a causal
+// mask and a few rows over a long cache all spread evenly.  A row tile whose units lie in
+// several CTAs leaves partials (two slots a CTA) that a second kernel joins in order.
+//
+// Inside a CTA the 256 rows are two M = 128 tiles that share keys and values:
+//   S_i = Q_i K^T  (tcgen05, K-major operands in 128-byte-swizzled shared memory)
+//   P_i = 2^(x - m) by four warps, one row a thread, bf16 back into TMEM over S_i
+//   O_i += P_i V   (A from TMEM, V as stored: MN-major)
+// in the order PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1): the tensor cores work on one tile while
+// the other's softmax runs.  The running maximum m of a row is only moved when a tile's
+// maximum passes it by 2^8 (the weights stay below 256, exact in the float32 sums), so O is
+// rescaled in TMEM a few times in a long row and not with every tile.
+// TMEM columns: S_0 0-127, S_1 128-255 (P_i in the first 64 of S_i), O_0 256.., O_1 384...
+// Warps 0-3 and 4-7: softmax and epilogue of tile 0 and 1; warp 8: MMA issue; warps 9, 10:
+// loads by cp.async (any page size, stride and order; tokens that no row sees become zeros).
+
+#include "paged_prefill.cuh"
+
+namespace echo {
+
+constexpr int PT_THREADS = 352;
+constexpr int PT_LOADERS = 64;
+constexpr int PT_KEYS = 128;
+constexpr int PT_ITEMS = 4;          // ring of row tiles in flight
+constexpr int PT_VM = 8;             // ring of the tiles' token masks
+
+// A row tile's part in this CTA's run.
+struct PtItem {
+  int b, kvh, s0, n, len, pre, r0, nr;
+  int first, lo, hi;                 // over its rows: smallest first token and lower end, past the last position
+  TileSpan span;
+  int i0, i1;                        // tiles of the span in this run
+  int elsewhere;                     // 1: begun in another CTA, 2: goes on in another
+  int c0;                            // CTA of its first unit
+};
+
+template <int D>
+struct PtShape {
+  static constexpr int ATOMS = D / 64;
+  static constexpr int QB = ATOMS * 128 * 128;         // bytes of a query tile (and of a key or value tile)
+  static constexpr int SLOTS = D == 128 ? 4 : 6;
+};
+
+struct PtShared {
+  uint64_t qfull[2], qempty[2], full[8], empty[8];
+  uint64_t sfull[2], pfull[2], pvdone[2], oempty[2];
+  uint64_t ifull[PT_ITEMS], iempty[PT_ITEMS], vmfull[PT_VM];
+  uint32_t tmem_base;
+  int fail;
+  uint32_t vm[PT_VM][4];
+  PtItem item[PT_ITEMS];
+  int64_t row[2][PT_KEYS];
+  long long warp[PT_THREADS / 32];
+  long long before;
+  int found;
+  int tiles[PF_MAX_B + 1];           // row tiles before each sequence
+};
+
+template <int D>
+constexpr size_t pt_smem() {
+  return 1024 + (size_t)(2 + PtShape<D>::SLOTS) * PtShape<D>::QB + sizeof(PtShared);
+}
+
+__device__ __forceinline__ void pt_cp_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void pt_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void pt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void pt_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void pt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float pt_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Bounded wait of a whole warp: the same answer in every lane, and the warp together again
+// (the .aligned TMEM instructions want that).
+__device__ __forceinline__ bool pt_wait(uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+// bits [a, b) of a word
+__device__ __forceinline__ uint32_t pt_bits(int a, int b) {
+  a = min(max(a, 0), 32);
+  b = min(max(b, 0), 32);
+  const uint32_t hi = b >= 32 ? 0xffffffffu : (1u << b) - 1u, lo = a >= 32 ? 0xffffffffu : (1u << a) - 1u;
+  return hi & ~lo;
+}
+
+// What the rows of row tile rt of sequence b see.  Lanes of a warp share the rows when
+// `lanes` is 32 (all of them call); one thread walks them alone when it is 1.
+__device__ __forceinline__ void pt_range(const PrefillParams &P, int b, int rt, PtItem &I, int lanes) {
+  const SeqRows R = seq_rows(P, b);
+  const int G = P.G;
+  I.b = b;
+  I.s0 = R.s0;
+  I.n = R.n;
+  I.len = paged_len(P.C, P.seq_len, b);
+  I.pre = P.prefix_len ? min(P.prefix_len[b], I.len) : 0;
+  I.r0 = rt * PF_ROWS;
+  I.nr = (int)min((int64_t)PF_ROWS, (int64_t)R.n * G - I.r0);
+  const int i0 = max(I.r0 / G, I.n - I.len), i1 = (I.r0 + I.nr - 1) / G;   // tokens of the tile at positions >= 0
+  const int p0 = I.len - I.n;
+  int first = 0, lo = 0;
+  if (i1 < i0) {                                          // no row of the tile is there
+    first = lo = 0x7fffffff;
+    I.pre = 0;
+  } else if (P.first_tok) {
+    first = lo = 0x7fffffff;
+    for (int i = i0 + (lanes > 1 ? (int)(threadIdx.x & 31) : 0); i <= i1; i += lanes) {
+      const int f = max(__ldg(P.first_tok + R.s0 + i), 0);
+      first = min(first, f);
+      lo = min(lo, P.window ? max(f, p0 + i - P.window + 1) : f);
+    }
+    if (lanes > 1) {
+      first = __reduce_min_sync(0xffffffffu, first);
+      lo = __reduce_min_sync(0xffffffffu, lo);
+    }
+  } else if (P.window) {
+    lo = max(0, p0 + i0 - P.window + 1);
+  }
+  I.first = first;
+  I.lo = lo;
+  I.hi = i1 < i0 ? 0 : p0 + i1 + 1;
+  I.span = tile_span(first, I.pre, lo, I.hi, PT_KEYS);
+  if (I.span.nA + I.span.nB == 0) I.span.nA = 1;          // nothing seen: one tile of zeros writes the empty rows
+}
+
+template <int D, int MOD>
+__global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const __grid_constant__ PrefillParams P) {
+  using Sh = PtShape<D>;
+  constexpr int QB = Sh::QB, ATOMS = Sh::ATOMS, SLOTS = Sh::SLOTS;
+  constexpr bool CAP = MOD & 1, BIAS = MOD & 2;
+  extern __shared__ unsigned char pt_raw[];
+  unsigned char *R = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(pt_raw) + 1023) & ~uintptr_t(1023));
+  PtShared &S = *reinterpret_cast<PtShared *>(R + (2 + SLOTS) * QB);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const echo_paged_kv_t &C = P.C;
+  const int Hkv = C.n_kv_heads, G = P.G;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.qfull[i], PT_LOADERS);
+      mbar_init(&S.qempty[i], 1);
+      mbar_init(&S.sfull[i], 1);
+      mbar_init(&S.pfull[i], 128);
+      mbar_init(&S.pvdone[i], 1);
+      mbar_init(&S.oempty[i], 128);
+    }
+    for (int i = 0; i < SLOTS; ++i) { mbar_init(&S.full[i], PT_LOADERS); mbar_init(&S.empty[i], 1); }
+    for (int i = 0; i < PT_ITEMS; ++i) { mbar_init(&S.ifull[i], 1); mbar_init(&S.iempty[i], 9); }
+    for (int i = 0; i < PT_VM; ++i) mbar_init(&S.vmfull[i], PT_LOADERS / 32);
+    S.fail = 0;
+    S.found = -1;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&S.tmem_base, 512);
+    tmem_relinquish();
+  }
+
+  // ---- row tiles before each sequence
+  {
+    int base = 0;
+    for (int b0 = 0; b0 < P.B; b0 += PT_THREADS) {
+      const int b = b0 + tid;
+      const int n = b < P.B ? (int)(((int64_t)seq_rows(P, b).n * G + PF_ROWS - 1) / PF_ROWS) : 0;
+      int v = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      __syncthreads();
+      if (lane == 31) S.warp[warp] = v;
+      __syncthreads();
+      int end = base + v;
+      for (int w = 0; w < PT_THREADS / 32; ++w) {
+        if (w < warp) end += (int)S.warp[w];
+        base += (int)S.warp[w];
+      }
+      if (b < P.B) S.tiles[b] = end - n;
+    }
+    __syncthreads();
+    if (tid == 0) S.tiles[P.B] = base;
+  }
+  __syncthreads();
+  const int ntiles = S.tiles[P.B];
+  auto seq_of = [&](int x) {                              // last sequence whose tiles begin at or before x
+    int a = 0, c = P.B - 1;
+    while (a < c) {
+      const int m = (a + c + 1) >> 1;
+      if (S.tiles[m] <= x) a = m; else c = m - 1;
+    }
+    return a;
+  };
+  auto units_of = [&](int x) -> long long {               // units of row tile x, over the KV heads
+    PtItem I;
+    const int b = seq_of(x);
+    pt_range(P, b, x - S.tiles[b], I, 1);
+    return (long long)(I.span.nA + I.span.nB) * Hkv;
+  };
+  long long mine = 0, keep = 0;
+  for (int x = tid; x < ntiles; x += PT_THREADS) {
+    keep = units_of(x);
+    mine += keep;
+  }
+  long long total = 0;
+  {
+    long long v = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) S.warp[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < PT_THREADS / 32; ++w) total += S.warp[w];
+  }
+  const long long per = max((total + gridDim.x - 1) / (long long)gridDim.x, 1ll);
+  const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
+  if (u0 < u1) {
+    long long base = 0;
+    for (int x0 = 0; x0 < ntiles; x0 += PT_THREADS) {
+      const int x = x0 + tid;
+      const long long n = x < ntiles ? (ntiles <= PT_THREADS ? keep : units_of(x)) : 0;
+      long long v = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      __syncthreads();
+      if (lane == 31) S.warp[warp] = v;
+      __syncthreads();
+      long long end = base + v;
+      for (int w = 0; w < PT_THREADS / 32; ++w) {
+        if (w < warp) end += S.warp[w];
+        base += S.warp[w];
+      }
+      if (end - n <= u0 && u0 < end) {
+        S.found = x;
+        S.before = end - n;
+      }
+      __syncthreads();
+      if (S.found >= 0) break;
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  const int nu = u0 < u1 ? (int)(u1 - u0) : 0;
+  bool ok = true;
+
+  if (nu == 0) {
+    if (tid == 0) P.rec[blockIdx.x * 8] = 0;
+  } else if (warp >= 9) {
+    // ---------------------------------------------------------------- loads --
+    const int lt = tid - 9 * 32, c = lt & 7, rr = lt >> 3;
+    const uint32_t sw = (uint32_t)(rr * 128 + ((c ^ (rr & 7)) << 4));
+    int xt = S.found, b = seq_of(xt), rt = xt - S.tiles[b];
+    PtItem I;
+    pt_range(P, b, rt, I, 32);
+    {
+      const int nt = I.span.nA + I.span.nB;
+      const long long off = u0 - S.before;
+      I.kvh = (int)(off / nt);
+      I.i0 = (int)(off % nt);
+      I.i1 = min(nt, I.i0 + nu);
+      I.elsewhere = (I.i0 > 0 ? 1 : 0) | (I.i1 < nt ? 2 : 0);
+      I.c0 = (int)((u0 - I.i0) / per);
+    }
+    if (lt == 0 && I.len < I.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
+    if (lt == 0) P.rec[blockIdx.x * 8] = 0;
+    int nitem = 0, nq[2] = {0, 0};
+    int i = I.i0;                                         // tile of unit x
+    // the row of token lt and lt + 64 of tile t0 as page-table entries, to be turned into offsets later
+    int32_t ent[2] = {-1, -1};
+    int tok[2] = {-1, -1};
+    auto fetch = [&](const PtItem &J, int t0) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int t = t0 + lt + 64 * k;
+        const bool some = t < J.len && t >= J.first && ((t >= J.lo && t < J.hi) || t < J.pre);
+        tok[k] = some ? t : -1;
+        ent[k] = some ? __ldg(C.page_table + (int64_t)J.b * C.max_pages + t / C.page_tokens) : -1;
+      }
+    };
+    auto settle = [&](int x) {                            // unit x's offsets and token mask
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        int64_t o = -1;
+        if (tok[k] >= 0) {
+          if (ent[k] < 0 || ent[k] >= C.n_pages) paged_fail(C.status, ECHO_ERR_PAGE);
+          else o = (int64_t)ent[k] * C.page_stride + (int64_t)(tok[k] % C.page_tokens) * C.row_stride;
+        }
+        S.row[x & 1][lt + 64 * k] = o;
+        const uint32_t m = __ballot_sync(0xffffffffu, o >= 0);
+        if (lane == 0) S.vm[x % PT_VM][2 * k + (lt >> 5)] = m;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.vmfull[x % PT_VM]);
+      asm volatile("bar.sync 3, 64;" ::: "memory");
+    };
+    auto publish = [&]() {                                // hand the item to the other warps
+      const int e = nitem % PT_ITEMS;
+      ok = ok && pt_wait(&S.iempty[e], ((nitem / PT_ITEMS) & 1) ^ 1);
+      if (ok && lt == 0) {
+        S.item[e] = I;
+        mbar_arrive(&S.ifull[e]);
+      }
+      ++nitem;
+    };
+    auto load_q = [&](int h) {
+      if (!pt_wait(&S.qempty[h], (nq[h] & 1) ^ 1)) { ok = false; return; }
+      ++nq[h];
+      unsigned char *dst = R + h * QB;
+      const __nv_bfloat16 *q = (const __nv_bfloat16 *)P.q + (int64_t)I.s0 * P.q_stride + (int64_t)I.kvh * G * D + c * 8;
+#pragma unroll 4
+      for (int k = 0; k < 16; ++k) {
+        const int r = h * 128 + rr + 8 * k;
+        const bool there = r < I.nr;
+        const int t = there ? (I.r0 + r) / G : 0, g = there ? (I.r0 + r) - t * G : 0;
+        const __nv_bfloat16 *src = q + (int64_t)t * P.q_stride + g * D;
+#pragma unroll
+        for (int a = 0; a < ATOMS; ++a)
+          cp_async_16(dst + a * 16384 + sw + k * 1024, src + a * 64, there ? 16u : 0u);
+      }
+      pt_cp_arrive(&S.qfull[h]);
+    };
+    auto load_kv = [&](int x, int which) {                // 0: keys, 1: values of unit x
+      const int g = 2 * x + which, sl = g % SLOTS;
+      if (!pt_wait(&S.empty[sl], ((g / SLOTS) & 1) ^ 1)) { ok = false; return; }
+      unsigned char *dst = R + (2 + sl) * QB;
+      const __nv_bfloat16 *src = (const __nv_bfloat16 *)(which ? C.v : C.k) + (int64_t)I.kvh * C.head_stride + c * 8;
+#pragma unroll 8
+      for (int k = 0; k < 16; ++k) {
+        const int64_t o = S.row[x & 1][rr + 8 * k];
+        const __nv_bfloat16 *p = src + (o >= 0 ? o : 0);
+#pragma unroll
+        for (int a = 0; a < ATOMS; ++a)
+          cp_async_16(dst + a * 16384 + sw + k * 1024, p + a * 64, o >= 0 ? 16u : 0u);
+      }
+      pt_cp_arrive(&S.full[sl]);
+    };
+    publish();
+    fetch(I, I.span.tile(i) * PT_KEYS);
+    settle(0);
+    bool fresh = true;
+    // after a failed wait the loop goes on without loads: the two warps still meet in settle()
+    for (int x = 0; x < nu; ++x) {
+      // the next unit's place, and its page-table entries on their way
+      const bool more = x + 1 < nu, same = i + 1 < I.i1;
+      PtItem J = I;
+      int ni = i + 1;
+      if (more && !same) {
+        if (J.kvh + 1 < Hkv) {
+          ++J.kvh;
+        } else {
+          J.kvh = 0;
+          ++xt;
+          while (b + 1 < P.B && S.tiles[b + 1] <= xt) ++b;
+          pt_range(P, b, xt - S.tiles[b], J, 32);
+          if (lt == 0 && J.len < J.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
+        }
+        const int nt = J.span.nA + J.span.nB;
+        J.i0 = 0;
+        J.i1 = min(nt, nu - (x + 1));
+        J.elsewhere = J.i1 < nt ? 2 : 0;
+        J.c0 = blockIdx.x;
+        ni = 0;
+      }
+      if (more) fetch(J, J.span.tile(ni) * PT_KEYS);
+      if (ok && fresh) load_q(0);
+      if (ok) load_kv(x, 0);
+      if (ok && fresh && I.nr > 128) load_q(1);
+      if (ok) load_kv(x, 1);
+      if (more) {
+        settle(x + 1);
+        fresh = !same;
+        I = J;
+        i = ni;
+        if (fresh) publish();
+      }
+    }
+    cp_async_wait_all();
+  } else if (warp == 8) {
+    // ------------------------------------------------------------------ MMA --
+    if (lane == 0) {
+      constexpr uint32_t id_qk = instr_desc(FMT_BF16, FMT_BF16, 0, 0, 128, 128);
+      constexpr uint32_t id_pv = instr_desc(FMT_BF16, FMT_BF16, 0, 1, 128, D);
+      int nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
+      auto qk = [&](int t, int x, bool first, bool last) {
+        if (first) {
+          if (!mbar_wait(&S.qfull[t], nq[t] & 1)) { ok = false; return; }
+          ++nq[t];
+        }
+        const int g = 2 * x, sl = g % SLOTS;
+        if (!mbar_wait(&S.full[sl], (g / SLOTS) & 1)) { ok = false; return; }
+        fence_proxy_async_smem();                         // the loaders' cp.async writes, for the tensor cores
+        tc_fence_after();
+        const uint64_t ad = smem_desc(smem_u32(R + t * QB), 16, 1024, LAYOUT_SW128);
+        const uint64_t bd = smem_desc(smem_u32(R + (2 + sl) * QB), 16, 1024, LAYOUT_SW128);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (uint32_t)((k >> 2) * 1024 + (k & 3) * 2);
+          mma_f16(tmem + 128u * t, ad + o, bd + o, id_qk, k ? 1u : 0u);
+        }
+        mma_commit(&S.sfull[t]);
+        if (last) mma_commit(&S.qempty[t]);
+      };
+      auto pv = [&](int t, int x, bool first) {
+        if (!mbar_wait(&S.pfull[t], np[t] & 1)) { ok = false; return; }
+        ++np[t];
+        if (first) {
+          if (no[t] && !mbar_wait(&S.oempty[t], (no[t] - 1) & 1)) { ok = false; return; }
+          ++no[t];
+        }
+        const int g = 2 * x + 1, sl = g % SLOTS;
+        if (!mbar_wait(&S.full[sl], (g / SLOTS) & 1)) { ok = false; return; }
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t sa = smem_u32(R + (2 + sl) * QB);
+#pragma unroll
+        for (int k = 0; k < PT_KEYS / 16; ++k)
+          pt_mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * k,
+                    smem_desc(sa + (uint32_t)(k * 2048), 128 * 128, 1024, LAYOUT_SW128), id_pv, (!first || k) ? 1u : 0u);
+        mma_commit(&S.pvdone[t]);
+      };
+      int nitem = 0, left = 0;
+      bool two = false;
+      auto take = [&]() {
+        const int e = nitem % PT_ITEMS;
+        if (!mbar_wait(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; return; }
+        left = S.item[e].i1 - S.item[e].i0;
+        two = S.item[e].nr > 128;
+        mbar_arrive(&S.iempty[e]);
+        ++nitem;
+      };
+      take();
+      bool first = true;                                  // unit x is its row tile's first
+      if (ok) {
+        qk(0, 0, true, left == 1);
+        if (ok && two) qk(1, 0, true, left == 1);
+        mma_commit(&S.empty[0]);
+      }
+      for (int x = 0; x < nu && ok; ++x) {
+        const bool more = x + 1 < nu, fresh = left == 1, two_x = two;
+        pv(0, x, first);
+        if (!ok) break;
+        if (more && !fresh) qk(0, x + 1, false, left == 2);
+        if (ok && two_x) pv(1, x, first);
+        if (!ok) break;
+        mma_commit(&S.empty[(2 * x + 1) % SLOTS]);
+        if (!more) break;
+        if (fresh) {
+          take();
+          if (ok) qk(0, x + 1, true, left == 1);
+        } else {
+          --left;
+        }
+        if (ok && two) qk(1, x + 1, fresh, left == 1);
+        if (!ok) break;
+        mma_commit(&S.empty[(2 * x + 2) % SLOTS]);
+        first = fresh;
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax --
+    const int t = warp >> 2;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = trow + 128u * t, to = trow + 256u + 128u * t;
+    const int r = t * 128 + (warp & 3) * 32 + lane;       // row of the row tile
+    const float aa = fmaxf(fabsf(P.f.a), 1e-37f);         // a scale of 0 keeps masked scores at -inf
+    const bool negate = P.f.a < 0.f;
+    int x = 0, nitem = 0, ns = 0;                         // units, row tiles and this tile's units so far
+    while (x < nu && ok) {
+      const int e = nitem % PT_ITEMS;
+      if (!pt_wait(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; break; }
+      ++nitem;
+      const PtItem &I = S.item[e];
+      const int i0 = I.i0, i1 = I.i1;
+      if (t == 1 && I.nr <= 128) {
+        x += i1 - i0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.iempty[e]);
+        continue;
+      }
+      const int len = I.len, n = I.n, nr = I.nr, r0 = I.r0, s0 = I.s0, kvh = I.kvh, elsewhere = I.elsewhere, c0 = I.c0;
+      const TileSpan span = I.span;
+      int pre = I.pre;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.iempty[e]);
+      const bool there = r < nr, some = t * 128 + (warp & 3) * 32 < nr;
+      const int tk = there ? (r0 + r) / G : 0, hd = there ? kvh * G + (r0 + r) - tk * G : 0;
+      int pos = len - n + tk, first = 0, lo = 0;
+      if (!there || pos < 0) {
+        first = lo = 0x7fffffff;
+        pos = -1;
+        pre = 0;
+      } else {
+        if (P.first_tok) first = max(__ldg(P.first_tok + s0 + tk), 0);
+        lo = P.window ? max(first, pos - P.window + 1) : first;
+      }
+      float slope = 0.f;
+      if (BIAS && there) slope = __ldg(P.slopes + hd) * kPgLog2e;
+      const float posf = (float)pos;
+      float m = -INFINITY, l = 0.f;
+      for (int i = i0; i < i1; ++i, ++x, ++ns) {
+        if (!pt_wait(&S.sfull[t], ns & 1)) { ok = false; break; }
+        tc_fence_after();
+        if (some) {
+          const int t0 = span.tile(i) * PT_KEYS;
+          float v[128];
+          {
+            uint32_t (*u)[32] = reinterpret_cast<uint32_t (*)[32]>(v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, u[k]);
+          }
+          if (!pt_wait(&S.vmfull[x % PT_VM], (x / PT_VM) & 1)) { ok = false; break; }
+          uint32_t vm[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) vm[k] = S.vm[x % PT_VM][k];
+          const bool whole = ((t0 >= lo && t0 + PT_KEYS - 1 <= pos) || (t0 >= first && t0 + PT_KEYS <= pre)) &&
+                             (vm[0] & vm[1] & vm[2] & vm[3]) == 0xffffffffu;
+          tmem_wait_ld();
+          if (CAP || BIAS) {
+#pragma unroll
+            for (int k = 0; k < 128; ++k) {
+              v[k] = CAP ? score_log2(P.f, v[k]) : v[k] * P.f.a;
+              if (BIAS) v[k] = fmaf(-slope, fabsf(posf - (float)(t0 + k)), v[k]);
+            }
+          } else if (negate) {
+#pragma unroll
+            for (int k = 0; k < 128; ++k) v[k] = -v[k];
+          }
+          if (!__all_sync(0xffffffffu, whole || !there)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int w0 = t0 + 32 * k;
+              const uint32_t w = (pt_bits(lo - w0, pos + 1 - w0) | pt_bits(first - w0, pre - w0)) & vm[k];
+#pragma unroll
+              for (int q = 0; q < 32; ++q) v[32 * k + q] = (w >> q) & 1u ? v[32 * k + q] : -INFINITY;
+            }
+          }
+          float mx4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int k = 4; k < 128; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], v[k]);
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          const float sc = (CAP || BIAS) ? 1.f : aa;
+          mx *= sc;
+          // move the maximum when it is passed by 2^8, or was none
+          const bool move = mx > m + 8.f || (m == -INFINITY && mx > -INFINITY);
+          if (i == i0) {
+            m = mx;
+          } else if (__any_sync(0xffffffffu, move)) {
+            const float nm = move ? mx : m;
+            const float corr = move ? pt_ex2(m - nm) : 1.f;
+            m = nm;
+            l *= corr;
+            if (!pt_wait(&S.pvdone[t], (ns - 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D; k += 16) {
+              uint32_t o[16];
+              pt_ld16(to + k, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * corr);
+              pt_st16(to + k, o);
+            }
+          }
+          const float z = m == -INFINITY ? 0.f : m;
+          // weights, rounded to bf16 for the product (half a step, 2^-9 of each); the sum takes
+          // the unrounded ones
+          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int q = 0; q < 32; q += 2) {
+              const float a = pt_ex2(fmaf(v[32 * k + q], sc, -z)), c = pt_ex2(fmaf(v[32 * k + q + 1], sc, -z));
+              l4[q & 2] += a;
+              l4[(q & 2) + 1] += c;
+              const __nv_bfloat162 h = __floats2bfloat162_rn(a, c);
+              pk[q >> 1] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            pt_st16(ts + 16 * k, pk);
+          }
+          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          pt_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&S.pfull[t]);
+      }
+      if (!ok) break;
+      // ---- epilogue
+      if (!pt_wait(&S.pvdone[t], (ns - 1) & 1)) { ok = false; break; }
+      tc_fence_after();
+      const bool done = elsewhere == 0;
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      const int64_t orow = (int64_t)(s0 + tk) * P.Hq + hd;
+      const int64_t prow = (int64_t)(2 * blockIdx.x + ((elsewhere & 1) ? 0 : 1)) * P.prows + r;
+      if (some) {
+#pragma unroll
+        for (int k = 0; k < D; k += 32) {
+          uint32_t o[32];
+          tmem_ld32(to + k, o);
+          tmem_wait_ld();
+          if (there) {
+            if (done) {
+              uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)P.out + orow * D + k);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * q + 2 * y]) * inv,
+                                                                 __uint_as_float(o[8 * q + 2 * y + 1]) * inv);
+                  w[y] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+              uint4 *dst = reinterpret_cast<uint4 *>(P.po + prow * D + k);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&S.oempty[t]);
+      if (there) {
+        if (done) P.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPgLn2;
+        else *reinterpret_cast<float2 *>(P.pml + prow * 2) = make_float2(m, l);
+      }
+      if (r == 0 && elsewhere == 1) {                      // a split row tile ends here: to be joined
+        int32_t *rec = P.rec + blockIdx.x * 8;
+        rec[1] = c0;
+        rec[2] = s0;
+        rec[3] = r0;
+        rec[4] = nr;
+        rec[5] = kvh;
+        rec[0] = 1;
+      }
+    }
+  }
+  if (!ok) S.fail = 1;                                    // a bounded wait gave up
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (S.fail && tid == 0) {
+    P.rec[blockIdx.x * 8] = 0;
+    paged_fail(C.status, ECHO_ERR_TIMEOUT);
+  }
+}
+
+// Joins the partials of the row tile that ends in CTA blockIdx.x, in the order of their units:
+// slot 1 of its first CTA, then slot 0 of the following ones.  A warp takes a row.
+template <int D>
+__global__ void __launch_bounds__(128) paged_prefill_join_kernel(const __grid_constant__ PrefillParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c1 = blockIdx.x;
+  const int32_t *rec = P.rec + c1 * 8;
+  if (rec[0] == 0) return;
+  const int c0 = rec[1], s0 = rec[2], r0 = rec[3], nr = rec[4], kvh = rec[5];
+  const int lane = threadIdx.x & 31;
+  constexpr int VL = D / 32;
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < nr; r += gridDim.y * 4) {
+    float M = -INFINITY, L = 0.f, v[VL];
+#pragma unroll
+    for (int i = 0; i < VL; ++i) v[i] = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+      const int64_t row = (int64_t)(2 * c + (c == c0 ? 1 : 0)) * P.prows + r;
+      const float2 ml = *reinterpret_cast<const float2 *>(P.pml + row * 2);
+      const float nm = fmaxf(M, ml.x), z = nm == -INFINITY ? 0.f : nm;
+      const float wa = exp2f(M - z), wb = exp2f(ml.x - z);
+      M = nm;
+      L = L * wa + ml.y * wb;
+      const float *o = P.po + row * D + lane * VL;
+#pragma unroll
+      for (int i = 0; i < VL; ++i) v[i] = v[i] * wa + o[i] * wb;
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    const int tk = (r0 + r) / P.G, hd = kvh * P.G + (r0 + r) % P.G;
+    const int64_t orow = (int64_t)(s0 + tk) * P.Hq + hd;
+    __nv_bfloat16 *dst = (__nv_bfloat16 *)P.out + orow * D + lane * VL;
+#pragma unroll
+    for (int i = 0; i < VL; i += 2)
+      *reinterpret_cast<__nv_bfloat162 *>(dst + i) = __floats2bfloat162_rn(v[i] * inv, v[i + 1] * inv);
+    if (lane == 0) P.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPgLn2;
+  }
+}
+
+template <int D, int MOD>
+static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
+  static_assert(pt_smem<D>() <= 227 * 1024, "fits an SM");
+  ECHO_CUDA_OK(cudaFuncSetAttribute(paged_prefill_tc_kernel<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)pt_smem<D>()));
+  const int grid = std::min(sm_count(), PF_MAX_CTAS);
+  paged_prefill_tc_kernel<D, MOD><<<grid, PT_THREADS, pt_smem<D>(), st>>>(P);
+  ECHO_LAUNCH_OK();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, std::max(1, std::min(16, P.prows / 16)));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // starts up while the first kernel ends
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  ECHO_CUDA_OK(cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D>, P));
+  return ECHO_OK;
+}
+
+template <int D>
+static echo_status_t launch_mod(PrefillParams &P, cudaStream_t st) {
+  const int mod = (P.f.capped ? 1 : 0) | (P.slopes ? 2 : 0);
+  return mod == 0 ? launch_tc<D, 0>(P, st)
+       : mod == 1 ? launch_tc<D, 1>(P, st)
+       : mod == 2 ? launch_tc<D, 2>(P, st)
+                  : launch_tc<D, 3>(P, st);
+}
+
+echo_status_t launch_prefill_tc(PrefillParams &P, cudaStream_t st) {
+  return P.C.head_dim == 128 ? launch_mod<128>(P, st) : launch_mod<64>(P, st);
+}
+
+}  // namespace echo
