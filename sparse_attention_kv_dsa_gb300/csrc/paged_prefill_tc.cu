@@ -331,12 +331,16 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       if (lane == 0) mbar_arrive(&S.vmfull[x % PT_VM]);
       asm volatile("bar.sync 3, 64;" ::: "memory");
     };
-    auto publish = [&]() {                                // hand the item to the other warps
+    // Hand the item to the other warps.  Only the warp that publishes waits for the entry: the
+    // other one could come after it had been taken again, and wait for a phase that needs it.
+    auto publish = [&]() {
       const int e = nitem % PT_ITEMS;
-      ok = ok && pt_wait(&S.iempty[e], ((nitem / PT_ITEMS) & 1) ^ 1);
-      if (ok && lt == 0) {
-        S.item[e] = I;
-        mbar_arrive(&S.ifull[e]);
+      if (warp == 9) {
+        ok = ok && pt_wait(&S.iempty[e], ((nitem / PT_ITEMS) & 1) ^ 1);
+        if (ok && lt == 0) {
+          S.item[e] = I;
+          mbar_arrive(&S.ifull[e]);
+        }
       }
       ++nitem;
     };
