@@ -40,7 +40,19 @@ inline bool paged_rows_ok(const void *p, int64_t stride, int dtype) {
   return !((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * paged_elem_size(dtype))) & 15);
 }
 
+// Division of 0 <= t < 2^31 by a fixed d: the high word of t * (floor(2^64 / d) + 1), whose
+// excess t * (1 - frac) / 2^64 stays below 1 / d.
+struct FastDiv {
+  uint64_t m;
+  int d;
+};
+inline FastDiv fast_div(int d) { return {d > 1 ? ~0ull / (uint64_t)d + 1 : 0ull, d}; }
+
 // ----------------------------------------------------------------- device parts --
+__device__ __forceinline__ int div_by(const FastDiv &f, int t) {
+  return f.d == 1 ? t : (int)__umul64hi((uint64_t)t, f.m);
+}
+
 __device__ __forceinline__ void paged_fail(int32_t *status, int32_t code) {
   if (status) atomicCAS(status, 0, code);
 }

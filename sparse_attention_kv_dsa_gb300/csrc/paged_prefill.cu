@@ -275,6 +275,7 @@ extern "C" echo_status_t echo_paged_attn_prefill(const echo_paged_kv_t *cache, c
   P.C = *cache;
   P.q = q; P.q_stride = q_stride; P.q_start = q_start; P.seq_len = seq_len;
   P.N = N; P.B = B; P.Hq = Hq; P.G = Hq / cache->n_kv_heads;
+  P.page = fast_div(cache->page_tokens); P.group = fast_div(P.G);
   if ((int64_t)N * P.G > 0x7fff0000ll) return ECHO_ERR_UNSUPPORTED;
   P.slopes = scores->slopes; P.window = scores->window;
   P.first_tok = scores->first_tok; P.prefix_len = scores->prefix_len;

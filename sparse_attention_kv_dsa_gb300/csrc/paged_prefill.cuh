@@ -11,6 +11,7 @@ struct PrefillParams {
   int64_t q_stride;
   const int32_t *q_start, *seq_len;
   int N, B, Hq, G;
+  FastDiv page, group;               // by page_tokens and by G
   const float *slopes;
   int window;
   const int32_t *first_tok, *prefix_len;

@@ -19,15 +19,21 @@
 // maximum passes it by 2^8 (the weights stay below 256, exact in the float32 sums), so O is
 // rescaled in TMEM a few times in a long row and not with every tile.
 // TMEM columns: S_0 0-127, S_1 128-255 (P_i in the first 64 of S_i), O_0 256.., O_1 384...
-// Warps 0-3 and 4-7: softmax and epilogue of tile 0 and 1; warp 8: MMA issue; warps 9, 10:
-// loads by cp.async (any page size, stride and order; tokens that no row sees become zeros).
+// Warps 0-3 and 4-7: softmax and epilogue of tile 0 and 1 (200 registers: a row's 128 scores
+// stay in registers); warp 8: MMA issue; warp 9: the walk and the keys; warp 10: the values;
+// warp 11: the queries.  A tile of the cache whose 128
+// tokens are all seen by some row comes by TMA, in boxes of the largest power of two of rows
+// that divides a page (8 or more, the period of the swizzle); the tiles at the ends of the
+// seen range, and pages that no box fits, by cp.async row by row, unseen tokens as zeros.
+
+#include <atomic>
+#include <cudaTypedefs.h>
 
 #include "paged_prefill.cuh"
 
 namespace echo {
 
-constexpr int PT_THREADS = 352;
-constexpr int PT_LOADERS = 64;
+constexpr int PT_THREADS = 384;      // three warpgroups of 168 registers: 200 + 200 + 104 after the split
 constexpr int PT_KEYS = 128;
 constexpr int PT_ITEMS = 4;          // ring of row tiles in flight
 constexpr int PT_VM = 8;             // ring of the tiles' token masks
@@ -57,7 +63,9 @@ struct PtShared {
   int fail;
   uint32_t vm[PT_VM][4];
   PtItem item[PT_ITEMS];
-  int64_t row[2][PT_KEYS];
+  int64_t row[2][PT_KEYS];           // of a unit's tokens: offset of the row (-1: not there), and page
+  int32_t page[2][PT_KEYS];
+  int kvh[2], t0[2], whole[2];       // of a unit: KV head, first token, every token there
   long long warp[PT_THREADS / 32];
   long long before;
   int found;
@@ -104,10 +112,66 @@ __device__ __forceinline__ float pt_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// One lane of the warp.  The compiler knows the branch for a single thread's: its TMA and MMA
+// instructions take their operands straight from uniform registers, where `lane == 0` made it
+// write a loop over the active lanes around each (an issue took some 100 cycles).
+__device__ __forceinline__ bool pt_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Bounded wait for a phase (about a second), rolled up: this kernel has thirty of them, and
+// unrolled polls made it 223 KB, more than the instruction cache holds.
+__device__ __forceinline__ bool pt_wait1(uint64_t *bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+    if ((i & 63u) == 0 && global_ns() - t0 > kWaitLimitNs) return false;
+  return true;
+}
 // Bounded wait of a whole warp: the same answer in every lane, and the warp together again
 // (the .aligned TMEM instructions want that).
 __device__ __forceinline__ bool pt_wait(uint64_t *bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  return __all_sync(0xffffffffu, pt_wait1(bar, parity));
+}
+__device__ __forceinline__ void pt_tma3(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void pt_tma4(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ float pt_max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Pairs of floats, one instruction for both.
+__device__ __forceinline__ uint64_t pt_pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void pt_split(uint64_t p, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t pt_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pt_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 // bits [a, b) of a word
 __device__ __forceinline__ uint32_t pt_bits(int a, int b) {
@@ -157,7 +221,11 @@ __device__ __forceinline__ void pt_range(const PrefillParams &P, int b, int rt, 
 }
 
 template <int D, int MOD>
-__global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const __grid_constant__ PrefillParams P) {
+__global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const __grid_constant__ PrefillParams P,
+                                                                        const __grid_constant__ CUtensorMap kmap,
+                                                                        const __grid_constant__ CUtensorMap vmap,
+                                                                        const __grid_constant__ CUtensorMap qmap,
+                                                                        int box, int qbox) {
   using Sh = PtShape<D>;
   constexpr int QB = Sh::QB, ATOMS = Sh::ATOMS, SLOTS = Sh::SLOTS;
   constexpr bool CAP = MOD & 1, BIAS = MOD & 2;
@@ -170,16 +238,16 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.qfull[i], PT_LOADERS);
+      mbar_init(&S.qfull[i], 32);
       mbar_init(&S.qempty[i], 1);
       mbar_init(&S.sfull[i], 1);
       mbar_init(&S.pfull[i], 128);
       mbar_init(&S.pvdone[i], 1);
       mbar_init(&S.oempty[i], 128);
     }
-    for (int i = 0; i < SLOTS; ++i) { mbar_init(&S.full[i], PT_LOADERS); mbar_init(&S.empty[i], 1); }
-    for (int i = 0; i < PT_ITEMS; ++i) { mbar_init(&S.ifull[i], 1); mbar_init(&S.iempty[i], 9); }
-    for (int i = 0; i < PT_VM; ++i) mbar_init(&S.vmfull[i], PT_LOADERS / 32);
+    for (int i = 0; i < SLOTS; ++i) { mbar_init(&S.full[i], 32); mbar_init(&S.empty[i], 1); }
+    for (int i = 0; i < PT_ITEMS; ++i) { mbar_init(&S.ifull[i], 1); mbar_init(&S.iempty[i], 10); }
+    for (int i = 0; i < PT_VM; ++i) mbar_init(&S.vmfull[i], 1);
     S.fail = 0;
     S.found = -1;
     fence_mbar_init();
@@ -283,153 +351,203 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
 
   if (nu == 0) {
     if (tid == 0) P.rec[blockIdx.x * 8] = 0;
-  } else if (warp >= 9) {
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // ---------------------------------------------------------------- loads --
-    const int lt = tid - 9 * 32, c = lt & 7, rr = lt >> 3;
-    const uint32_t sw = (uint32_t)(rr * 128 + ((c ^ (rr & 7)) << 4));
-    int xt = S.found, b = seq_of(xt), rt = xt - S.tiles[b];
-    PtItem I;
-    pt_range(P, b, rt, I, 32);
-    {
-      const int nt = I.span.nA + I.span.nB;
-      const long long off = u0 - S.before;
-      I.kvh = (int)(off / nt);
-      I.i0 = (int)(off % nt);
-      I.i1 = min(nt, I.i0 + nu);
-      I.elsewhere = (I.i0 > 0 ? 1 : 0) | (I.i1 < nt ? 2 : 0);
-      I.c0 = (int)((u0 - I.i0) / per);
-    }
-    if (lt == 0 && I.len < I.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
-    if (lt == 0) P.rec[blockIdx.x * 8] = 0;
-    int nitem = 0, nq[2] = {0, 0};
-    int i = I.i0;                                         // tile of unit x
-    // the row of token lt and lt + 64 of tile t0 as page-table entries, to be turned into offsets later
-    int32_t ent[2] = {-1, -1};
-    int tok[2] = {-1, -1};
-    auto fetch = [&](const PtItem &J, int t0) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int t = t0 + lt + 64 * k;
-        const bool some = t < J.len && t >= J.first && ((t >= J.lo && t < J.hi) || t < J.pre);
-        tok[k] = some ? t : -1;
-        ent[k] = some ? __ldg(C.page_table + (int64_t)J.b * C.max_pages + t / C.page_tokens) : -1;
-      }
-    };
-    auto settle = [&](int x) {                            // unit x's offsets and token mask
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        int64_t o = -1;
-        if (tok[k] >= 0) {
-          if (ent[k] < 0 || ent[k] >= C.n_pages) paged_fail(C.status, ECHO_ERR_PAGE);
-          else o = (int64_t)ent[k] * C.page_stride + (int64_t)(tok[k] % C.page_tokens) * C.row_stride;
-        }
-        S.row[x & 1][lt + 64 * k] = o;
-        const uint32_t m = __ballot_sync(0xffffffffu, o >= 0);
-        if (lane == 0) S.vm[x % PT_VM][2 * k + (lt >> 5)] = m;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.vmfull[x % PT_VM]);
-      asm volatile("bar.sync 3, 64;" ::: "memory");
-    };
-    // Hand the item to the other warps.  Only the warp that publishes waits for the entry: the
-    // other one could come after it had been taken again, and wait for a phase that needs it.
-    auto publish = [&]() {
-      const int e = nitem % PT_ITEMS;
-      if (warp == 9) {
-        ok = ok && pt_wait(&S.iempty[e], ((nitem / PT_ITEMS) & 1) ^ 1);
-        if (ok && lt == 0) {
-          S.item[e] = I;
-          mbar_arrive(&S.ifull[e]);
-        }
-      }
-      ++nitem;
-    };
-    auto load_q = [&](int h) {
-      if (!pt_wait(&S.qempty[h], (nq[h] & 1) ^ 1)) { ok = false; return; }
-      ++nq[h];
-      unsigned char *dst = R + h * QB;
-      const __nv_bfloat16 *q = (const __nv_bfloat16 *)P.q + (int64_t)I.s0 * P.q_stride + (int64_t)I.kvh * G * D + c * 8;
-#pragma unroll 4
-      for (int k = 0; k < 16; ++k) {
-        const int r = h * 128 + rr + 8 * k;
-        const bool there = r < I.nr;
-        const int t = there ? (I.r0 + r) / G : 0, g = there ? (I.r0 + r) - t * G : 0;
-        const __nv_bfloat16 *src = q + (int64_t)t * P.q_stride + g * D;
-#pragma unroll
-        for (int a = 0; a < ATOMS; ++a)
-          cp_async_16(dst + a * 16384 + sw + k * 1024, src + a * 64, there ? 16u : 0u);
-      }
-      pt_cp_arrive(&S.qfull[h]);
-    };
-    auto load_kv = [&](int x, int which) {                // 0: keys, 1: values of unit x
-      const int g = 2 * x + which, sl = g % SLOTS;
+    // warp 9: the walk over the units, and the keys; warp 10: the values; warp 11: the queries
+    int issued = 0;                                       // stages of the key and value ring begun, by this warp
+    auto load_tile = [&](int g, int x, const CUtensorMap *map, const void *base) {
+      const int sl = g % SLOTS, e = x & 1, t0 = S.t0[e], kvh = S.kvh[e];
       if (!pt_wait(&S.empty[sl], ((g / SLOTS) & 1) ^ 1)) { ok = false; return; }
       unsigned char *dst = R + (2 + sl) * QB;
-      const __nv_bfloat16 *src = (const __nv_bfloat16 *)(which ? C.v : C.k) + (int64_t)I.kvh * C.head_stride + c * 8;
-#pragma unroll 8
-      for (int k = 0; k < 16; ++k) {
-        const int64_t o = S.row[x & 1][rr + 8 * k];
-        const __nv_bfloat16 *p = src + (o >= 0 ? o : 0);
+      if (box && S.whole[e]) {
+        if (lane == 0) mbar_arrive_expect_tx(&S.full[sl], QB);
+        else mbar_arrive(&S.full[sl]);
+        const int nb = PT_KEYS / box;
+        const int tj = t0 + min(lane, nb - 1) * box;      // box `lane`: its page and first row
+        const int pg = S.page[e][tj - t0], rj = tj - div_by(P.page, tj) * C.page_tokens;
+        __syncwarp();
+#pragma unroll 4
+        for (int j = 0; j < nb; ++j) {
+          const int p = __shfl_sync(0xffffffffu, pg, j), r = __shfl_sync(0xffffffffu, rj, j);
+          if (pt_elect()) {
 #pragma unroll
-        for (int a = 0; a < ATOMS; ++a)
-          cp_async_16(dst + a * 16384 + sw + k * 1024, p + a * 64, o >= 0 ? 16u : 0u);
-      }
-      pt_cp_arrive(&S.full[sl]);
-    };
-    publish();
-    fetch(I, I.span.tile(i) * PT_KEYS);
-    settle(0);
-    bool fresh = true;
-    // after a failed wait the loop goes on without loads: the two warps still meet in settle()
-    for (int x = 0; x < nu; ++x) {
-      // the next unit's place, and its page-table entries on their way
-      const bool more = x + 1 < nu, same = i + 1 < I.i1;
-      PtItem J = I;
-      int ni = i + 1;
-      if (more && !same) {
-        if (J.kvh + 1 < Hkv) {
-          ++J.kvh;
-        } else {
-          J.kvh = 0;
-          ++xt;
-          while (b + 1 < P.B && S.tiles[b + 1] <= xt) ++b;
-          pt_range(P, b, xt - S.tiles[b], J, 32);
-          if (lt == 0 && J.len < J.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
+            for (int a = 0; a < ATOMS; ++a)
+              pt_tma4(dst + a * 16384 + j * box * 128, map, &S.full[sl], a * 64, r, kvh, p);
+          }
         }
-        const int nt = J.span.nA + J.span.nB;
-        J.i0 = 0;
-        J.i1 = min(nt, nu - (x + 1));
-        J.elsewhere = J.i1 < nt ? 2 : 0;
-        J.c0 = blockIdx.x;
-        ni = 0;
+        __syncwarp();
+      } else {
+        const int c = lane & 7, rr = lane >> 3;
+        const __nv_bfloat16 *src = (const __nv_bfloat16 *)base + (int64_t)kvh * C.head_stride + c * 8;
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+          const int r = rr + 4 * k;
+          const int64_t o = S.row[e][r];
+          const __nv_bfloat16 *p = src + (o >= 0 ? o : 0);
+#pragma unroll
+          for (int a = 0; a < ATOMS; ++a)
+            cp_async_16(dst + a * 16384 + r * 128 + ((c ^ (r & 7)) << 4), p + a * 64, o >= 0 ? 16u : 0u);
+        }
+        pt_cp_arrive(&S.full[sl]);
       }
-      if (more) fetch(J, J.span.tile(ni) * PT_KEYS);
-      if (ok && fresh) load_q(0);
-      if (ok) load_kv(x, 0);
-      if (ok && fresh && I.nr > 128) load_q(1);
-      if (ok) load_kv(x, 1);
-      if (more) {
-        settle(x + 1);
-        fresh = !same;
-        I = J;
-        i = ni;
-        if (fresh) publish();
+      issued = g + 1;
+    };
+    if (warp == 9) {
+      int xt = S.found, b = seq_of(xt);
+      PtItem I;
+      pt_range(P, b, xt - S.tiles[b], I, 32);
+      {
+        const int nt = I.span.nA + I.span.nB;
+        const long long off = u0 - S.before;
+        I.kvh = (int)(off / nt);
+        I.i0 = (int)(off - (long long)I.kvh * nt);
+        I.i1 = min(nt, I.i0 + nu);
+        I.elsewhere = (I.i0 > 0 ? 1 : 0) | (I.i1 < nt ? 2 : 0);
+        I.c0 = (int)((u0 - I.i0) / per);
       }
+      if (lane == 0) {
+        if (I.len < I.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
+        P.rec[blockIdx.x * 8] = 0;
+      }
+      int nitem = 0, i = I.i0;                            // i: tile of the unit looked up next
+      int32_t ent[4];
+      int tok[4];
+      for (int x = -1; x < nu; ++x) {
+        // unit x + 1: its row tile, and its tokens' page-table entries on their way
+        const bool more = x + 1 < nu;
+        if (more) {
+          const bool fresh = x < 0 || i == I.i1;
+          if (x >= 0 && fresh) {
+            if (I.kvh + 1 < Hkv) {
+              ++I.kvh;
+            } else {
+              I.kvh = 0;
+              ++xt;
+              while (b + 1 < P.B && S.tiles[b + 1] <= xt) ++b;
+              pt_range(P, b, xt - S.tiles[b], I, 32);
+              if (lane == 0 && I.len < I.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
+            }
+            const int nt = I.span.nA + I.span.nB;
+            I.i0 = i = 0;
+            I.i1 = min(nt, nu - (x + 1));
+            I.elsewhere = I.i1 < nt ? 2 : 0;
+            I.c0 = blockIdx.x;
+          }
+          if (fresh) {                                    // hand it to the other warps
+            const int e = nitem % PT_ITEMS;
+            ok = ok && pt_wait(&S.iempty[e], ((nitem / PT_ITEMS) & 1) ^ 1);
+            if (ok && lane == 0) {
+              S.item[e] = I;
+              mbar_arrive(&S.ifull[e]);
+            }
+            ++nitem;
+          }
+          const int t0 = I.span.tile(i) * PT_KEYS;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int t = t0 + lane + 32 * k;
+            const bool some = t < I.len && t >= I.first && ((t >= I.lo && t < I.hi) || t < I.pre);
+            tok[k] = some ? t : -1;
+            ent[k] = some ? __ldg(C.page_table + (int64_t)I.b * C.max_pages + div_by(P.page, t)) : -1;
+          }
+        }
+        if (x >= 0 && ok) load_tile(2 * x, x, &kmap, C.k);
+        if (more) {                                       // unit x + 1's offsets and token mask
+          const int e = (x + 1) & 1, v = (x + 1) % PT_VM;
+          uint32_t all = 0xffffffffu;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            int64_t o = -1;
+            if (tok[k] >= 0) {
+              if (ent[k] < 0 || ent[k] >= C.n_pages) paged_fail(C.status, ECHO_ERR_PAGE);
+              else o = (int64_t)ent[k] * C.page_stride +
+                       (int64_t)(tok[k] - div_by(P.page, tok[k]) * C.page_tokens) * C.row_stride;
+            }
+            S.row[e][lane + 32 * k] = o;
+            S.page[e][lane + 32 * k] = ent[k];
+            const uint32_t m = __ballot_sync(0xffffffffu, o >= 0);
+            all &= m;
+            if (lane == 0) S.vm[v][k] = m;
+          }
+          if (lane == 0) {
+            S.kvh[e] = I.kvh;
+            S.t0[e] = I.span.tile(i) * PT_KEYS;
+            S.whole[e] = all == 0xffffffffu;
+            mbar_arrive(&S.vmfull[v]);
+          }
+          ++i;
+          asm volatile("bar.sync 3, 64;" ::: "memory");   // warp 10 has unit x + 1
+        }
+        // after a failed wait the walk goes on without loads: warp 10 still meets its barriers
+      }
+    } else if (warp == 10) {
+      for (int x = 0; x < nu; ++x) {
+        asm volatile("bar.sync 3, 64;" ::: "memory");
+        if (ok) load_tile(2 * x + 1, x, &vmap, C.v);
+      }
+    } else if (warp == 11) {
+      int nq[2] = {0, 0}, nitem = 0;
+      for (int x = 0; x < nu && ok;) {
+        const int e = nitem % PT_ITEMS;
+        if (!pt_wait(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; break; }
+        ++nitem;
+        const int s0 = S.item[e].s0, r0 = S.item[e].r0, nr = S.item[e].nr, kvh = S.item[e].kvh;
+        x += S.item[e].i1 - S.item[e].i0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.iempty[e]);
+        for (int h = 0; h < (nr > 128 ? 2 : 1) && ok; ++h) {
+          if (!pt_wait(&S.qempty[h], (nq[h] & 1) ^ 1)) { ok = false; break; }
+          ++nq[h];
+          unsigned char *dst = R + h * QB;
+          if (qbox) {                                     // G divides 128: whole tokens
+            if (lane == 0) mbar_arrive_expect_tx(&S.qfull[h], QB);
+            else mbar_arrive(&S.qfull[h]);
+            __syncwarp();
+            if (pt_elect()) {
+#pragma unroll
+              for (int a = 0; a < ATOMS; ++a)
+                pt_tma3(dst + a * 16384, &qmap, &S.qfull[h], a * 64, kvh * G, s0 + div_by(P.group, r0 + 128 * h));
+            }
+            __syncwarp();
+          } else {
+            const int c = lane & 7;
+            const __nv_bfloat16 *q = (const __nv_bfloat16 *)P.q + (int64_t)s0 * P.q_stride + (int64_t)kvh * G * D + c * 8;
+#pragma unroll 4
+            for (int k = 0; k < 32; ++k) {
+              const int r = (lane >> 3) + 4 * k, rt = h * 128 + r;
+              const bool there = rt < nr;
+              const int t = there ? div_by(P.group, r0 + rt) : 0, gh = there ? r0 + rt - t * G : 0;
+              const __nv_bfloat16 *src = q + (int64_t)t * P.q_stride + gh * D;
+#pragma unroll
+              for (int a = 0; a < ATOMS; ++a)
+                cp_async_16(dst + a * 16384 + r * 128 + ((c ^ (r & 7)) << 4), src + a * 64, there ? 16u : 0u);
+            }
+            pt_cp_arrive(&S.qfull[h]);
+          }
+        }
+      }
+      for (int h = 0; !ok && h < 2; ++h)
+        if (nq[h]) pt_wait(&S.qfull[h], (nq[h] - 1) & 1);
     }
-    cp_async_wait_all();
-  } else if (warp == 8) {
+    if (warp >= 9) {
+      cp_async_wait_all();
+      // after a failed wait, the copies in flight land before the CTA ends (bounded waits)
+      for (int g = max(0, issued - SLOTS); !ok && g < issued; ++g)
+        if ((g & 1) == (warp == 10 ? 1 : 0)) pt_wait(&S.full[g % SLOTS], (g / SLOTS) & 1);
+    }
+    if (warp == 8 && pt_elect()) {
     // ------------------------------------------------------------------ MMA --
-    if (lane == 0) {
       constexpr uint32_t id_qk = instr_desc(FMT_BF16, FMT_BF16, 0, 0, 128, 128);
       constexpr uint32_t id_pv = instr_desc(FMT_BF16, FMT_BF16, 0, 1, 128, D);
       int nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
       auto qk = [&](int t, int x, bool first, bool last) {
         if (first) {
-          if (!mbar_wait(&S.qfull[t], nq[t] & 1)) { ok = false; return; }
+          if (!pt_wait1(&S.qfull[t], nq[t] & 1)) { ok = false; return; }
           ++nq[t];
         }
         const int g = 2 * x, sl = g % SLOTS;
-        if (!mbar_wait(&S.full[sl], (g / SLOTS) & 1)) { ok = false; return; }
+        if (!pt_wait1(&S.full[sl], (g / SLOTS) & 1)) { ok = false; return; }
         fence_proxy_async_smem();                         // the loaders' cp.async writes, for the tensor cores
         tc_fence_after();
         const uint64_t ad = smem_desc(smem_u32(R + t * QB), 16, 1024, LAYOUT_SW128);
@@ -443,14 +561,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         if (last) mma_commit(&S.qempty[t]);
       };
       auto pv = [&](int t, int x, bool first) {
-        if (!mbar_wait(&S.pfull[t], np[t] & 1)) { ok = false; return; }
+        if (!pt_wait1(&S.pfull[t], np[t] & 1)) { ok = false; return; }
         ++np[t];
         if (first) {
-          if (no[t] && !mbar_wait(&S.oempty[t], (no[t] - 1) & 1)) { ok = false; return; }
+          if (no[t] && !pt_wait1(&S.oempty[t], (no[t] - 1) & 1)) { ok = false; return; }
           ++no[t];
         }
         const int g = 2 * x + 1, sl = g % SLOTS;
-        if (!mbar_wait(&S.full[sl], (g / SLOTS) & 1)) { ok = false; return; }
+        if (!pt_wait1(&S.full[sl], (g / SLOTS) & 1)) { ok = false; return; }
         fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t sa = smem_u32(R + (2 + sl) * QB);
@@ -464,7 +582,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       bool two = false;
       auto take = [&]() {
         const int e = nitem % PT_ITEMS;
-        if (!mbar_wait(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; return; }
+        if (!pt_wait1(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; return; }
         left = S.item[e].i1 - S.item[e].i0;
         two = S.item[e].nr > 128;
         mbar_arrive(&S.iempty[e]);
@@ -500,12 +618,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     }
   } else {
     // -------------------------------------------------------------- softmax --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int t = warp >> 2;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = trow + 128u * t, to = trow + 256u + 128u * t;
     const int r = t * 128 + (warp & 3) * 32 + lane;       // row of the row tile
-    const float aa = fmaxf(fabsf(P.f.a), 1e-37f);         // a scale of 0 keeps masked scores at -inf
-    const bool negate = P.f.a < 0.f;
+    const float aa = fmaxf(P.f.a, 1e-37f);                // a scale of 0 keeps masked scores at -inf
     int x = 0, nitem = 0, ns = 0;                         // units, row tiles and this tile's units so far
     while (x < nu && ok) {
       const int e = nitem % PT_ITEMS;
@@ -525,7 +643,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.iempty[e]);
       const bool there = r < nr, some = t * 128 + (warp & 3) * 32 < nr;
-      const int tk = there ? (r0 + r) / G : 0, hd = there ? kvh * G + (r0 + r) - tk * G : 0;
+      const int tk = there ? div_by(P.group, r0 + r) : 0, hd = there ? kvh * G + (r0 + r) - tk * G : 0;
       int pos = len - n + tk, first = 0, lo = 0;
       if (!there || pos < 0) {
         first = lo = 0x7fffffff;
@@ -536,7 +654,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         lo = P.window ? max(first, pos - P.window + 1) : first;
       }
       float slope = 0.f;
-      if (BIAS && there) slope = __ldg(P.slopes + hd) * kPgLog2e;
+      if (BIAS && P.slopes && there) slope = __ldg(P.slopes + hd) * kPgLog2e;
       const float posf = (float)pos;
       float m = -INFINITY, l = 0.f;
       for (int i = i0; i < i1; ++i, ++x, ++ns) {
@@ -563,9 +681,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
               v[k] = CAP ? score_log2(P.f, v[k]) : v[k] * P.f.a;
               if (BIAS) v[k] = fmaf(-slope, fabsf(posf - (float)(t0 + k)), v[k]);
             }
-          } else if (negate) {
-#pragma unroll
-            for (int k = 0; k < 128; ++k) v[k] = -v[k];
           }
           if (!__all_sync(0xffffffffu, whole || !there)) {
 #pragma unroll
@@ -578,7 +693,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           }
           float mx4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-          for (int k = 4; k < 128; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], v[k]);
+          for (int k = 4; k < 124; k += 8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx4[q] = pt_max3(mx4[q], v[k + 2 * q], v[k + 2 * q + 1]);
+          }
+          mx4[0] = pt_max3(mx4[0], v[124], v[125]);
+          mx4[1] = pt_max3(mx4[1], v[126], v[127]);
           float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float sc = (CAP || BIAS) ? 1.f : aa;
           mx *= sc;
@@ -593,7 +713,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
             l *= corr;
             if (!pt_wait(&S.pvdone[t], (ns - 1) & 1)) { ok = false; break; }
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D; k += 16) {
               uint32_t o[16];
               pt_ld16(to + k, o);
@@ -606,21 +726,28 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           const float z = m == -INFINITY ? 0.f : m;
           // weights, rounded to bf16 for the product (half a step, 2^-9 of each); the sum takes
           // the unrounded ones
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sc2 = pt_pair(sc, sc), z2 = pt_pair(-z, -z);
+          uint64_t l2[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t pk[16];
 #pragma unroll
             for (int q = 0; q < 32; q += 2) {
-              const float a = pt_ex2(fmaf(v[32 * k + q], sc, -z)), c = pt_ex2(fmaf(v[32 * k + q + 1], sc, -z));
-              l4[q & 2] += a;
-              l4[(q & 2) + 1] += c;
+              float a, c;
+              pt_split(pt_fma2(pt_pair(v[32 * k + q], v[32 * k + q + 1]), sc2, z2), a, c);
+              a = pt_ex2(a);
+              c = pt_ex2(c);
+              l2[(q >> 1) & 3] = pt_add2(l2[(q >> 1) & 3], pt_pair(a, c));
               const __nv_bfloat162 h = __floats2bfloat162_rn(a, c);
               pk[q >> 1] = *reinterpret_cast<const uint32_t *>(&h);
             }
             pt_st16(ts + 16 * k, pk);
           }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          {
+            float a, c;
+            pt_split(pt_add2(pt_add2(l2[0], l2[1]), pt_add2(l2[2], l2[3])), a, c);
+            l += a + c;
+          }
           pt_wait_st();
         }
         tc_fence_before();
@@ -635,7 +762,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       const int64_t orow = (int64_t)(s0 + tk) * P.Hq + hd;
       const int64_t prow = (int64_t)(2 * blockIdx.x + ((elsewhere & 1) ? 0 : 1)) * P.prows + r;
       if (some) {
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < D; k += 32) {
           uint32_t o[32];
           tmem_ld32(to + k, o);
@@ -727,13 +854,59 @@ __global__ void __launch_bounds__(128) paged_prefill_join_kernel(const __grid_co
   }
 }
 
+// A bf16 tensor of `nd` dimensions with 128-byte-swizzled boxes of 64 innermost values; strides
+// in values, of all but the innermost dimension.  False where a stride is none that a tensor
+// map takes (the loads then go row by row).
+static bool bf16_map(CUtensorMap *m, const void *base, int nd, const int64_t *dims, const int64_t *strides, const int *box) {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 enc = fn.load(std::memory_order_acquire);
+  if (!enc) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
+        qr != cudaDriverEntryPointSuccess)
+      return false;
+    enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    fn.store(enc, std::memory_order_release);
+  }
+  cuuint64_t ds[4], st[3];
+  cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < nd; ++i) {
+    ds[i] = (cuuint64_t)dims[i];
+    bx[i] = (cuuint32_t)box[i];
+    if (i + 1 < nd) {
+      if (strides[i] <= 0 || strides[i] >= (1ll << 38)) return false;
+      st[i] = (cuuint64_t)strides[i] * 2;
+    }
+  }
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)nd, const_cast<void *>(base), ds, st, bx, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int MOD>
 static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
   static_assert(pt_smem<D>() <= 227 * 1024, "fits an SM");
   ECHO_CUDA_OK(cudaFuncSetAttribute(paged_prefill_tc_kernel<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)pt_smem<D>()));
+  int box = std::min(P.C.page_tokens & -P.C.page_tokens, PT_KEYS), qbox = 128 % P.G == 0 ? 128 / P.G : 0;
+  CUtensorMap kmap = {}, vmap = {}, qmap = {};
+  {
+    // pages [page][head][row][value], boxes of `box` rows; the stride of a dimension of one
+    // entry is never used: any that is valid will do
+    const echo_paged_kv_t &C = P.C;
+    const int64_t dims[4] = {D, C.page_tokens, C.n_kv_heads, C.n_pages};
+    const int64_t st[3] = {C.page_tokens > 1 ? C.row_stride : D, C.n_kv_heads > 1 ? C.head_stride : D,
+                           C.n_pages > 1 ? C.page_stride : D};
+    const int bx[4] = {64, box, 1, 1};
+    if (box < 8 || !bf16_map(&kmap, C.k, 4, dims, st, bx) || !bf16_map(&vmap, C.v, 4, dims, st, bx)) box = 0;
+    // queries [token][head][value], boxes of 128 packed rows
+    const int64_t qd[3] = {D, P.Hq, P.N}, qs[2] = {D, P.N > 1 ? P.q_stride : D};
+    const int qb[3] = {64, P.G, qbox};
+    if (qbox && !bf16_map(&qmap, P.q, 3, qd, qs, qb)) qbox = 0;
+  }
   const int grid = std::min(sm_count(), PF_MAX_CTAS);
-  paged_prefill_tc_kernel<D, MOD><<<grid, PT_THREADS, pt_smem<D>(), st>>>(P);
+  paged_prefill_tc_kernel<D, MOD><<<grid, PT_THREADS, pt_smem<D>(), st>>>(P, kmap, vmap, qmap, box, qbox);
   ECHO_LAUNCH_OK();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, std::max(1, std::min(16, P.prows / 16)));
@@ -750,7 +923,8 @@ static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
 
 template <int D>
 static echo_status_t launch_mod(PrefillParams &P, cudaStream_t st) {
-  const int mod = (P.f.capped ? 1 : 0) | (P.slopes ? 2 : 0);
+  // a negative scale goes with the bias: the plain form takes the largest raw product
+  const int mod = (P.f.capped ? 1 : 0) | (P.slopes || P.f.a < 0.f ? 2 : 0);
   return mod == 0 ? launch_tc<D, 0>(P, st)
        : mod == 1 ? launch_tc<D, 1>(P, st)
        : mod == 2 ? launch_tc<D, 2>(P, st)
