@@ -284,6 +284,7 @@ extern "C" echo_status_t echo_paged_attn_prefill(const echo_paged_kv_t *cache, c
   cudaStream_t cs = (cudaStream_t)stream;
   if (cache->dtype == ECHO_BF16) {
     P.prows = prefill_prows(N, P.G);
+    P.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
     P.po = reinterpret_cast<float *>(workspace);
     P.pml = P.po + (size_t)2 * PF_MAX_CTAS * P.prows * cache->head_dim;
     P.rec = reinterpret_cast<int32_t *>(P.pml + (size_t)2 * PF_MAX_CTAS * P.prows * 2);

@@ -21,6 +21,7 @@ struct PrefillParams {
   float *po, *pml;                   // partials [2 CTAs][rows][d], [2 CTAs][rows][2]
   int32_t *rec;                      // [CTAs][8]: the split row tile that ends in the CTA
   int prows;                         // rows of a partial
+  int wide;                          // out is 32-byte aligned
 };
 
 // Rows of sequence b: [s0, s0 + n).

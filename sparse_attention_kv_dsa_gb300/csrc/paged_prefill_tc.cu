@@ -5,8 +5,9 @@
 //
 // A persistent CTA per SM.  The work is dealt out in units -- one 128-token tile of the cache
 // for one row tile of 256 packed rows (token r / G, head r % G of the KV head's group) --
-// ordered by (sequence, row tile, KV head, tile); every CTA takes an equal run of them, found
-// from the device's own lengths and masks, so that ragged prompts, the triangle of a causal
+// ordered by (sequence, row tile, KV head, tile); every CTA takes a run of them of equal
+// weight (a row tile begins with PT_ITEM_WEIGHT units' worth: its queries, its epilogue),
+// found from the device's own lengths and masks, so that ragged prompts, the triangle of a causal
 // mask and a few rows over a long cache all spread evenly.  A row tile whose units lie in
 // several CTAs leaves partials (two slots a CTA) that a second kernel joins in order.
 //
@@ -37,13 +38,14 @@ constexpr int PT_THREADS = 384;      // three warpgroups of 168 registers: 200 +
 constexpr int PT_KEYS = 128;
 constexpr int PT_ITEMS = 4;          // ring of row tiles in flight
 constexpr int PT_VM = 8;             // ring of the tiles' token masks
+constexpr int PT_ITEM_WEIGHT = 1;    // of a row tile besides its tiles, in units
 
 // A row tile's part in this CTA's run.
 struct PtItem {
   int b, kvh, s0, n, len, pre, r0, nr;
   int first, lo, hi;                 // over its rows: smallest first token and lower end, past the last position
   TileSpan span;
-  int i0, i1;                        // tiles of the span in this run
+  int i0, i1;                        // tiles of the span in this run; i1 < 0: the run is over
   int elsewhere;                     // 1: begun in another CTA, 2: goes on in another
   int c0;                            // CTA of its first unit
 };
@@ -58,14 +60,15 @@ struct PtShape {
 struct PtShared {
   uint64_t qfull[2], qempty[2], full[8], empty[8];
   uint64_t sfull[2], pfull[2], pvdone[2], oempty[2];
-  uint64_t ifull[PT_ITEMS], iempty[PT_ITEMS], vmfull[PT_VM];
+  uint64_t ifull[PT_ITEMS], iempty[PT_ITEMS];
   uint32_t tmem_base;
   int fail;
-  uint32_t vm[PT_VM][4];
+  uint32_t vm[PT_VM][4];             // tokens there, of unit x in entry x % PT_VM
+  uint32_t vmtag[PT_VM];             // 2 (x + 1) + (all of them there)
   PtItem item[PT_ITEMS];
   int64_t row[2][PT_KEYS];           // of a unit's tokens: offset of the row (-1: not there), and page
   int32_t page[2][PT_KEYS];
-  int kvh[2], t0[2], whole[2];       // of a unit: KV head, first token, every token there
+  int kvh[2], t0[2], whole[2];       // of a unit: KV head (-1: no more units), first token, every token there
   long long warp[PT_THREADS / 32];
   long long before;
   int found;
@@ -165,13 +168,26 @@ __device__ __forceinline__ void pt_split(uint64_t p, float &a, float &b) {
 }
 __device__ __forceinline__ uint64_t pt_fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 __device__ __forceinline__ uint64_t pt_add2(uint64_t a, uint64_t b) {
   uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+__device__ __forceinline__ void pt_release(uint32_t *p, uint32_t v) {
+  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t pt_acquire(const uint32_t *p) {
+  uint32_t v;
+  asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void pt_store32(void *p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 // bits [a, b) of a word
 __device__ __forceinline__ uint32_t pt_bits(int a, int b) {
@@ -247,7 +263,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     }
     for (int i = 0; i < SLOTS; ++i) { mbar_init(&S.full[i], 32); mbar_init(&S.empty[i], 1); }
     for (int i = 0; i < PT_ITEMS; ++i) { mbar_init(&S.ifull[i], 1); mbar_init(&S.iempty[i], 10); }
-    for (int i = 0; i < PT_VM; ++i) mbar_init(&S.vmfull[i], 1);
+    for (int i = 0; i < PT_VM; ++i) S.vmtag[i] = 0;
     S.fail = 0;
     S.found = -1;
     fence_mbar_init();
@@ -292,11 +308,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     }
     return a;
   };
-  auto units_of = [&](int x) -> long long {               // units of row tile x, over the KV heads
+  auto units_of = [&](int x) -> long long {               // weight of row tile x, over the KV heads
     PtItem I;
     const int b = seq_of(x);
     pt_range(P, b, x - S.tiles[b], I, 1);
-    return (long long)(I.span.nA + I.span.nB) * Hkv;
+    return (long long)(I.span.nA + I.span.nB + PT_ITEM_WEIGHT) * Hkv;
   };
   long long mine = 0, keep = 0;
   for (int x = tid; x < ntiles; x += PT_THREADS) {
@@ -346,12 +362,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
-  const int nu = u0 < u1 ? (int)(u1 - u0) : 0;
   bool ok = true;
 
-  if (nu == 0) {
-    if (tid == 0) P.rec[blockIdx.x * 8] = 0;
-  } else if (warp >= 8) {
+  if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // ---------------------------------------------------------------- loads --
     // warp 9: the walk over the units, and the keys; warp 10: the values; warp 11: the queries
@@ -394,55 +407,64 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       issued = g + 1;
     };
     if (warp == 9) {
-      int xt = S.found, b = seq_of(xt);
-      PtItem I;
-      pt_range(P, b, xt - S.tiles[b], I, 32);
-      {
+      int xt = S.found, b = 0, nitem = 0, i = 0;          // i: tile of the unit looked up next
+      PtItem I = {};
+      long long ws = 0;                                   // weight before the row tile
+      auto run_of = [&](int i0) {                         // the row tile's tiles in this run; none: the run is over
         const int nt = I.span.nA + I.span.nB;
-        const long long off = u0 - S.before;
-        I.kvh = (int)(off / nt);
-        I.i0 = (int)(off - (long long)I.kvh * nt);
-        I.i1 = min(nt, I.i0 + nu);
+        I.i0 = i0;
+        I.i1 = (int)min((long long)nt, u1 - ws - PT_ITEM_WEIGHT);
         I.elsewhere = (I.i0 > 0 ? 1 : 0) | (I.i1 < nt ? 2 : 0);
-        I.c0 = (int)((u0 - I.i0) / per);
+        I.c0 = (int)((ws + PT_ITEM_WEIGHT) / per);
+        if (I.i1 <= I.i0) I.i1 = -1;
+        i = i0;
+      };
+      auto hand_over = [&]() {                            // the row tile, to the other warps
+        const int e = nitem % PT_ITEMS;
+        ok = ok && pt_wait(&S.iempty[e], ((nitem / PT_ITEMS) & 1) ^ 1);
+        if (ok && lane == 0) {
+          S.item[e] = I;
+          mbar_arrive(&S.ifull[e]);
+        }
+        ++nitem;
+      };
+      auto enter = [&]() {                                // row tile xt
+        while (b + 1 < P.B && S.tiles[b + 1] <= xt) ++b;
+        pt_range(P, b, xt - S.tiles[b], I, 32);
+        if (lane == 0 && I.len < I.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
+      };
+      if (lane == 0) P.rec[blockIdx.x * 8] = 0;
+      if (xt >= 0) {
+        b = seq_of(xt);
+        enter();
+        const int nt = I.span.nA + I.span.nB + PT_ITEM_WEIGHT;
+        I.kvh = (int)((u0 - S.before) / nt);
+        ws = S.before + (long long)I.kvh * nt;
+        run_of(max(0, (int)(u0 - ws) - PT_ITEM_WEIGHT));
+      } else {
+        I.i1 = -1;
       }
-      if (lane == 0) {
-        if (I.len < I.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
-        P.rec[blockIdx.x * 8] = 0;
-      }
-      int nitem = 0, i = I.i0;                            // i: tile of the unit looked up next
+      hand_over();
       int32_t ent[4];
       int tok[4];
-      for (int x = -1; x < nu; ++x) {
+      for (int x = -1;; ++x) {
         // unit x + 1: its row tile, and its tokens' page-table entries on their way
-        const bool more = x + 1 < nu;
+        if (x >= 0 && i == I.i1) {
+          ws += I.span.nA + I.span.nB + PT_ITEM_WEIGHT;
+          if (I.kvh + 1 < Hkv) {
+            ++I.kvh;
+            run_of(0);
+          } else if (++xt < ntiles) {
+            I.kvh = 0;
+            enter();
+            run_of(0);
+          } else {
+            I.i1 = -1;
+          }
+          hand_over();
+        }
+        const bool more = I.i1 >= 0;
         if (more) {
-          const bool fresh = x < 0 || i == I.i1;
-          if (x >= 0 && fresh) {
-            if (I.kvh + 1 < Hkv) {
-              ++I.kvh;
-            } else {
-              I.kvh = 0;
-              ++xt;
-              while (b + 1 < P.B && S.tiles[b + 1] <= xt) ++b;
-              pt_range(P, b, xt - S.tiles[b], I, 32);
-              if (lane == 0 && I.len < I.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
-            }
-            const int nt = I.span.nA + I.span.nB;
-            I.i0 = i = 0;
-            I.i1 = min(nt, nu - (x + 1));
-            I.elsewhere = I.i1 < nt ? 2 : 0;
-            I.c0 = blockIdx.x;
-          }
-          if (fresh) {                                    // hand it to the other warps
-            const int e = nitem % PT_ITEMS;
-            ok = ok && pt_wait(&S.iempty[e], ((nitem / PT_ITEMS) & 1) ^ 1);
-            if (ok && lane == 0) {
-              S.item[e] = I;
-              mbar_arrive(&S.ifull[e]);
-            }
-            ++nitem;
-          }
           const int t0 = I.span.tile(i) * PT_KEYS;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -453,8 +475,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           }
         }
         if (x >= 0 && ok) load_tile(2 * x, x, &kmap, C.k);
+        const int e = (x + 1) & 1, v = (x + 1) % PT_VM;
         if (more) {                                       // unit x + 1's offsets and token mask
-          const int e = (x + 1) & 1, v = (x + 1) % PT_VM;
           uint32_t all = 0xffffffffu;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -474,28 +496,32 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
             S.kvh[e] = I.kvh;
             S.t0[e] = I.span.tile(i) * PT_KEYS;
             S.whole[e] = all == 0xffffffffu;
-            mbar_arrive(&S.vmfull[v]);
+            pt_release(&S.vmtag[v], 2u * (uint32_t)(x + 2) + (all == 0xffffffffu ? 1u : 0u));
           }
           ++i;
-          asm volatile("bar.sync 3, 64;" ::: "memory");   // warp 10 has unit x + 1
+        } else if (lane == 0) {
+          S.kvh[e] = -1;
         }
+        asm volatile("bar.sync 3, 64;" ::: "memory");     // warp 10 has unit x + 1
+        if (!more) break;
         // after a failed wait the walk goes on without loads: warp 10 still meets its barriers
       }
     } else if (warp == 10) {
-      for (int x = 0; x < nu; ++x) {
+      for (int x = 0;; ++x) {
         asm volatile("bar.sync 3, 64;" ::: "memory");
+        if (S.kvh[x & 1] < 0) break;
         if (ok) load_tile(2 * x + 1, x, &vmap, C.v);
       }
     } else if (warp == 11) {
       int nq[2] = {0, 0}, nitem = 0;
-      for (int x = 0; x < nu && ok;) {
+      while (ok) {
         const int e = nitem % PT_ITEMS;
         if (!pt_wait(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; break; }
         ++nitem;
-        const int s0 = S.item[e].s0, r0 = S.item[e].r0, nr = S.item[e].nr, kvh = S.item[e].kvh;
-        x += S.item[e].i1 - S.item[e].i0;
+        const int s0 = S.item[e].s0, r0 = S.item[e].r0, nr = S.item[e].nr, kvh = S.item[e].kvh, i1 = S.item[e].i1;
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.iempty[e]);
+        if (i1 < 0) break;
         for (int h = 0; h < (nr > 128 ? 2 : 1) && ok; ++h) {
           if (!pt_wait(&S.qempty[h], (nq[h] & 1) ^ 1)) { ok = false; break; }
           ++nq[h];
@@ -578,42 +604,41 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
                     smem_desc(sa + (uint32_t)(k * 2048), 128 * 128, 1024, LAYOUT_SW128), id_pv, (!first || k) ? 1u : 0u);
         mma_commit(&S.pvdone[t]);
       };
-      int nitem = 0, left = 0;
+      int nitem = 0, left = 0;                            // units of the row tile from unit x on
       bool two = false;
-      auto take = [&]() {
+      auto take = [&]() {                                 // the next row tile; false: no more
         const int e = nitem % PT_ITEMS;
-        if (!pt_wait1(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; return; }
-        left = S.item[e].i1 - S.item[e].i0;
+        if (!pt_wait1(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; return false; }
+        const int i1 = S.item[e].i1;
+        left = i1 - S.item[e].i0;
         two = S.item[e].nr > 128;
         mbar_arrive(&S.iempty[e]);
         ++nitem;
+        return i1 >= 0;
       };
-      take();
-      bool first = true;                                  // unit x is its row tile's first
-      if (ok) {
+      if (take()) {
         qk(0, 0, true, left == 1);
         if (ok && two) qk(1, 0, true, left == 1);
-        mma_commit(&S.empty[0]);
-      }
-      for (int x = 0; x < nu && ok; ++x) {
-        const bool more = x + 1 < nu, fresh = left == 1, two_x = two;
-        pv(0, x, first);
-        if (!ok) break;
-        if (more && !fresh) qk(0, x + 1, false, left == 2);
-        if (ok && two_x) pv(1, x, first);
-        if (!ok) break;
-        mma_commit(&S.empty[(2 * x + 1) % SLOTS]);
-        if (!more) break;
-        if (fresh) {
-          take();
-          if (ok) qk(0, x + 1, true, left == 1);
-        } else {
-          --left;
+        if (ok) mma_commit(&S.empty[0]);
+        bool first = true;                                // unit x is its row tile's first
+        for (int x = 0; ok; ++x) {
+          const bool fresh = left == 1, two_x = two;      // fresh: unit x + 1 begins a row tile
+          pv(0, x, first);
+          if (ok && !fresh) qk(0, x + 1, false, left == 2);
+          if (ok && two_x) pv(1, x, first);
+          if (!ok) break;
+          mma_commit(&S.empty[(2 * x + 1) % SLOTS]);
+          if (fresh) {
+            if (!take()) break;
+            qk(0, x + 1, true, left == 1);
+          } else {
+            --left;
+          }
+          if (ok && two) qk(1, x + 1, fresh, left == 1);
+          if (!ok) break;
+          mma_commit(&S.empty[(2 * x + 2) % SLOTS]);
+          first = fresh;
         }
-        if (ok && two) qk(1, x + 1, fresh, left == 1);
-        if (!ok) break;
-        mma_commit(&S.empty[(2 * x + 2) % SLOTS]);
-        first = fresh;
       }
     }
   } else {
@@ -625,12 +650,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     const int r = t * 128 + (warp & 3) * 32 + lane;       // row of the row tile
     const float aa = fmaxf(P.f.a, 1e-37f);                // a scale of 0 keeps masked scores at -inf
     int x = 0, nitem = 0, ns = 0;                         // units, row tiles and this tile's units so far
-    while (x < nu && ok) {
+    while (ok) {
       const int e = nitem % PT_ITEMS;
       if (!pt_wait(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; break; }
       ++nitem;
       const PtItem &I = S.item[e];
       const int i0 = I.i0, i1 = I.i1;
+      if (i1 < 0) break;
       if (t == 1 && I.nr <= 128) {
         x += i1 - i0;
         __syncwarp();
@@ -656,24 +682,26 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       float slope = 0.f;
       if (BIAS && P.slopes && there) slope = __ldg(P.slopes + hd) * kPgLog2e;
       const float posf = (float)pos;
+      // tiles that every row of the warp sees whole: by its window, and by its prefix
+      const int wa = __reduce_max_sync(0xffffffffu, there ? (int)(((unsigned)lo + PT_KEYS - 1) / PT_KEYS) : 0);
+      const int wb = __reduce_min_sync(0xffffffffu, there ? (pos + 1) / PT_KEYS : 0x7fffffff);
+      const int pa = __reduce_max_sync(0xffffffffu, there ? (int)(((unsigned)first + PT_KEYS - 1) / PT_KEYS) : 0);
+      const int pb = __reduce_min_sync(0xffffffffu, there ? pre / PT_KEYS : 0x7fffffff);
       float m = -INFINITY, l = 0.f;
       for (int i = i0; i < i1; ++i, ++x, ++ns) {
         if (!pt_wait(&S.sfull[t], ns & 1)) { ok = false; break; }
         tc_fence_after();
         if (some) {
-          const int t0 = span.tile(i) * PT_KEYS;
+          const int ti = span.tile(i), t0 = ti * PT_KEYS;
           float v[128];
           {
             uint32_t (*u)[32] = reinterpret_cast<uint32_t (*)[32]>(v);
 #pragma unroll
             for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, u[k]);
           }
-          if (!pt_wait(&S.vmfull[x % PT_VM], (x / PT_VM) & 1)) { ok = false; break; }
-          uint32_t vm[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) vm[k] = S.vm[x % PT_VM][k];
-          const bool whole = ((t0 >= lo && t0 + PT_KEYS - 1 <= pos) || (t0 >= first && t0 + PT_KEYS <= pre)) &&
-                             (vm[0] & vm[1] & vm[2] & vm[3]) == 0xffffffffu;
+          // the tile's token mask: written before its keys were loaded, so it is there
+          uint32_t tag = pt_acquire(&S.vmtag[x % PT_VM]);
+          const bool whole = ((ti >= wa && ti < wb) || (ti >= pa && ti < pb)) && tag == 2u * (uint32_t)(x + 1) + 1u;
           tmem_wait_ld();
           if (CAP || BIAS) {
 #pragma unroll
@@ -682,11 +710,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
               if (BIAS) v[k] = fmaf(-slope, fabsf(posf - (float)(t0 + k)), v[k]);
             }
           }
-          if (!__all_sync(0xffffffffu, whole || !there)) {
+          if (!whole) {                                   // the same in every lane
+            for (uint32_t k = 0; (tag >> 1) != (uint32_t)(x + 1) && k < (1u << 20); ++k) tag = pt_acquire(&S.vmtag[x % PT_VM]);
+            if ((tag >> 1) != (uint32_t)(x + 1)) S.fail = 1;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int w0 = t0 + 32 * k;
-              const uint32_t w = (pt_bits(lo - w0, pos + 1 - w0) | pt_bits(first - w0, pre - w0)) & vm[k];
+              const uint32_t w = (pt_bits(lo - w0, pos + 1 - w0) | pt_bits(first - w0, pre - w0)) & S.vm[x % PT_VM][k];
 #pragma unroll
               for (int q = 0; q < 32; ++q) v[32 * k + q] = (w >> q) & 1u ? v[32 * k + q] : -INFINITY;
             }
@@ -703,12 +733,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           const float sc = (CAP || BIAS) ? 1.f : aa;
           mx *= sc;
           // move the maximum when it is passed by 2^8, or was none
-          const bool move = mx > m + 8.f || (m == -INFINITY && mx > -INFINITY);
+          const float nm = mx > m + 8.f ? mx : m;
           if (i == i0) {
             m = mx;
-          } else if (__any_sync(0xffffffffu, move)) {
-            const float nm = move ? mx : m;
-            const float corr = move ? pt_ex2(m - nm) : 1.f;
+          } else if (__any_sync(0xffffffffu, nm != m)) {
+            const float corr = nm != m ? pt_ex2(m - nm) : 1.f;
             m = nm;
             l *= corr;
             if (!pt_wait(&S.pvdone[t], (ns - 1) & 1)) { ok = false; break; }
@@ -769,17 +798,22 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           tmem_wait_ld();
           if (there) {
             if (done) {
-              uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)P.out + orow * D + k);
+              __nv_bfloat16 *dst = (__nv_bfloat16 *)P.out + orow * D + k;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t w[4];
+              for (int q = 0; q < 2; ++q) {
+                uint32_t w[8];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * q + 2 * y]) * inv,
-                                                                 __uint_as_float(o[8 * q + 2 * y + 1]) * inv);
+                for (int y = 0; y < 8; ++y) {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[16 * q + 2 * y]) * inv,
+                                                                 __uint_as_float(o[16 * q + 2 * y + 1]) * inv);
                   w[y] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                if (P.wide) {                              // whole 32-byte sectors
+                  pt_store32(dst + 16 * q, w);
+                } else {
+                  reinterpret_cast<uint4 *>(dst + 16 * q)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                  reinterpret_cast<uint4 *>(dst + 16 * q)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
               }
             } else {
               uint4 *dst = reinterpret_cast<uint4 *>(P.po + prow * D + k);
