@@ -21,11 +21,13 @@
 // rescaled in TMEM a few times in a long row and not with every tile.
 // TMEM columns: S_0 0-127, S_1 128-255 (P_i in the first 64 of S_i), O_0 256.., O_1 384...
 // Warps 0-3 and 4-7: softmax and epilogue of tile 0 and 1 (200 registers: a row's 128 scores
-// stay in registers); warp 8: MMA issue; warp 9: the walk and the keys; warp 10: the values;
-// warp 11: the queries.  A tile of the cache whose 128
+// stay in registers); warp 8: MMA issue; warp 9: the walk over the units and their page-table
+// look-ups; warp 10: the queries; warps 12, 13: the keys; 14, 15: the values.  A tile of the cache whose 128
 // tokens are all seen by some row comes by TMA, in boxes of the largest power of two of rows
 // that divides a page (8 or more, the period of the swizzle); the tiles at the ends of the
-// seen range, and pages that no box fits, by cp.async row by row, unseen tokens as zeros.
+// seen range, and pages that no box fits, by cp.async row by row, unseen tokens as zeros.  A
+// warp gets a TMA instruction away every 105 cycles whatever its box (measured), so two warps
+// share a tile: 16-row pages need 16 boxes of it.
 
 #include <atomic>
 #include <cudaTypedefs.h>
@@ -34,9 +36,10 @@
 
 namespace echo {
 
-constexpr int PT_THREADS = 384;      // three warpgroups of 168 registers: 200 + 200 + 104 after the split
+constexpr int PT_THREADS = 512;      // four warpgroups of 128 registers: 200 + 200 + 64 + 48 after the split
 constexpr int PT_KEYS = 128;
 constexpr int PT_ITEMS = 4;          // ring of row tiles in flight
+constexpr int PT_UNITS = 4;          // ring of units looked up
 constexpr int PT_VM = 8;             // ring of the tiles' token masks
 constexpr int PT_ITEM_WEIGHT = 1;    // of a row tile besides its tiles, in units
 
@@ -60,15 +63,15 @@ struct PtShape {
 struct PtShared {
   uint64_t qfull[2], qempty[2], full[8], empty[8];
   uint64_t sfull[2], pfull[2], pvdone[2], oempty[2];
-  uint64_t ifull[PT_ITEMS], iempty[PT_ITEMS];
+  uint64_t ifull[PT_ITEMS], iempty[PT_ITEMS], ufull[PT_UNITS], uempty[PT_UNITS];
   uint32_t tmem_base;
   int fail;
   uint32_t vm[PT_VM][4];             // tokens there, of unit x in entry x % PT_VM
   uint32_t vmtag[PT_VM];             // 2 (x + 1) + (all of them there)
   PtItem item[PT_ITEMS];
-  int64_t row[2][PT_KEYS];           // of a unit's tokens: offset of the row (-1: not there), and page
-  int32_t page[2][PT_KEYS];
-  int kvh[2], t0[2], whole[2];       // of a unit: KV head (-1: no more units), first token, every token there
+  int64_t row[PT_UNITS][PT_KEYS];           // of a unit's tokens: offset of the row (-1: not there), and page
+  int32_t page[PT_UNITS][PT_KEYS];
+  int kvh[PT_UNITS], t0[PT_UNITS], whole[PT_UNITS];       // of a unit: KV head (-1: no more units), first token, every token there
   long long warp[PT_THREADS / 32];
   long long before;
   int found;
@@ -123,14 +126,19 @@ __device__ __forceinline__ bool pt_elect() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// Bounded wait for a phase (about a second), rolled up: this kernel has thirty of them, and
-// unrolled polls made it 223 KB, more than the instruction cache holds.
+// Bounded wait for a phase (a second from the 64th poll on).  Rolled up: this kernel has thirty
+// of them, and unrolled polls made it 223 KB, more than the instruction cache holds.  The
+// global timer is only read when the wait is long: it takes 200 cycles.
 __device__ __forceinline__ bool pt_wait1(uint64_t *bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
+  uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
-    if ((i & 63u) == 0 && global_ns() - t0 > kWaitLimitNs) return false;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 63u) == 0) {
+      const uint64_t t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) return false;
+    }
+  }
   return true;
 }
 // Bounded wait of a whole warp: the same answer in every lane, and the warp together again
@@ -261,8 +269,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       mbar_init(&S.pvdone[i], 1);
       mbar_init(&S.oempty[i], 128);
     }
-    for (int i = 0; i < SLOTS; ++i) { mbar_init(&S.full[i], 32); mbar_init(&S.empty[i], 1); }
+    for (int i = 0; i < SLOTS; ++i) { mbar_init(&S.full[i], 64); mbar_init(&S.empty[i], 1); }
     for (int i = 0; i < PT_ITEMS; ++i) { mbar_init(&S.ifull[i], 1); mbar_init(&S.iempty[i], 10); }
+    for (int i = 0; i < PT_UNITS; ++i) { mbar_init(&S.ufull[i], 1); mbar_init(&S.uempty[i], 4); }
     for (int i = 0; i < PT_VM; ++i) S.vmtag[i] = 0;
     S.fail = 0;
     S.found = -1;
@@ -365,47 +374,62 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
   bool ok = true;
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    // ---------------------------------------------------------------- loads --
-    // warp 9: the walk over the units, and the keys; warp 10: the values; warp 11: the queries
-    int issued = 0;                                       // stages of the key and value ring begun, by this warp
-    auto load_tile = [&](int g, int x, const CUtensorMap *map, const void *base) {
-      const int sl = g % SLOTS, e = x & 1, t0 = S.t0[e], kvh = S.kvh[e];
-      if (!pt_wait(&S.empty[sl], ((g / SLOTS) & 1) ^ 1)) { ok = false; return; }
-      unsigned char *dst = R + (2 + sl) * QB;
-      if (box && S.whole[e]) {
-        if (lane == 0) mbar_arrive_expect_tx(&S.full[sl], QB);
-        else mbar_arrive(&S.full[sl]);
-        const int nb = PT_KEYS / box;
-        const int tj = t0 + min(lane, nb - 1) * box;      // box `lane`: its page and first row
-        const int pg = S.page[e][tj - t0], rj = tj - div_by(P.page, tj) * C.page_tokens;
-        __syncwarp();
+    if (warp >= 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+      // -------------------------------------------------------- keys, values --
+      const int which = (warp - 12) >> 1, half = warp & 1;
+      const CUtensorMap *map = which ? &vmap : &kmap;
+      const int nbox = box ? PT_KEYS / box : 0, jb = nbox > 1 ? half * (nbox >> 1) : 0;
+      const int je = nbox > 1 ? jb + (nbox >> 1) : (half ? 0 : nbox);      // this warp's boxes
+      int issued = 0;
+      for (int x = 0;; ++x) {
+        const int e = x % PT_UNITS, g = 2 * x + which, sl = g % SLOTS;
+        if (!pt_wait(&S.ufull[e], (x / PT_UNITS) & 1)) { ok = false; break; }
+        const int kvh = S.kvh[e];
+        if (kvh < 0) break;
+        if (!pt_wait(&S.empty[sl], ((g / SLOTS) & 1) ^ 1)) { ok = false; break; }
+        unsigned char *dst = R + (2 + sl) * QB;
+        if (S.whole[e]) {
+          if (lane == 0 && je > jb) mbar_arrive_expect_tx(&S.full[sl], (je - jb) * box * 128 * ATOMS);
+          else mbar_arrive(&S.full[sl]);
+          const int j = min(jb + lane, PT_KEYS / box - 1), tj = S.t0[e] + j * box;     // box jb + lane
+          const int pg = S.page[e][j * box], rj = tj - div_by(P.page, tj) * C.page_tokens;
+          __syncwarp();
+#pragma unroll 2
+          for (int q = jb; q < je; ++q) {
+            const int pq = __shfl_sync(0xffffffffu, pg, q - jb), rq = __shfl_sync(0xffffffffu, rj, q - jb);
+            if (pt_elect()) {
+#pragma unroll
+              for (int a = 0; a < ATOMS; ++a)
+                pt_tma4(dst + a * 16384 + q * box * 128, map, &S.full[sl], a * 64, rq, kvh, pq);
+            }
+          }
+          __syncwarp();
+        } else {
+          const int c = lane & 7;
+          const __nv_bfloat16 *src = (const __nv_bfloat16 *)(which ? C.v : C.k) + (int64_t)kvh * C.head_stride + c * 8;
 #pragma unroll 4
-        for (int j = 0; j < nb; ++j) {
-          const int p = __shfl_sync(0xffffffffu, pg, j), r = __shfl_sync(0xffffffffu, rj, j);
-          if (pt_elect()) {
+          for (int k = 0; k < 16; ++k) {
+            const int r = half * 64 + (lane >> 3) + 4 * k;
+            const int64_t o = S.row[e][r];
+            const __nv_bfloat16 *p = src + (o >= 0 ? o : 0);
 #pragma unroll
             for (int a = 0; a < ATOMS; ++a)
-              pt_tma4(dst + a * 16384 + j * box * 128, map, &S.full[sl], a * 64, r, kvh, p);
+              cp_async_16(dst + a * 16384 + r * 128 + ((c ^ (r & 7)) << 4), p + a * 64, o >= 0 ? 16u : 0u);
           }
+          pt_cp_arrive(&S.full[sl]);
+          __syncwarp();
         }
-        __syncwarp();
-      } else {
-        const int c = lane & 7, rr = lane >> 3;
-        const __nv_bfloat16 *src = (const __nv_bfloat16 *)base + (int64_t)kvh * C.head_stride + c * 8;
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-          const int r = rr + 4 * k;
-          const int64_t o = S.row[e][r];
-          const __nv_bfloat16 *p = src + (o >= 0 ? o : 0);
-#pragma unroll
-          for (int a = 0; a < ATOMS; ++a)
-            cp_async_16(dst + a * 16384 + r * 128 + ((c ^ (r & 7)) << 4), p + a * 64, o >= 0 ? 16u : 0u);
-        }
-        pt_cp_arrive(&S.full[sl]);
+        if (lane == 0) mbar_arrive(&S.uempty[e]);
+        issued = g + 1;
       }
-      issued = g + 1;
-    };
+      cp_async_wait_all();
+      // after a failed wait, the copies in flight land before the CTA ends (bounded waits)
+      for (int g = max(which, issued + 1 - SLOTS); !ok && g < issued; g += 2)
+        pt_wait(&S.full[g % SLOTS], (g / SLOTS) & 1);
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // ------------------------------------------------------------ walk, queries --
     if (warp == 9) {
       int xt = S.found, b = 0, nitem = 0, i = 0;          // i: tile of the unit looked up next
       PtItem I = {};
@@ -445,11 +469,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         I.i1 = -1;
       }
       hand_over();
-      int32_t ent[4];
-      int tok[4];
-      for (int x = -1;; ++x) {
-        // unit x + 1: its row tile, and its tokens' page-table entries on their way
-        if (x >= 0 && i == I.i1) {
+      // unit x is entered (its row tile handed over) and its page-table entries fetched while
+      // unit x - 1's are turned into offsets
+      int32_t ent[4] = {-1, -1, -1, -1}, pent[4];
+      int t0 = 0, pt0 = 0, pkvh = -1;
+      uint32_t seen = 0, pseen = 0;                       // bit k: token t0 + lane + 32 k is seen by some row
+      for (int x = 0;; ++x) {
+        if (x > 0 && I.i1 >= 0 && i == I.i1) {
           ws += I.span.nA + I.span.nB + PT_ITEM_WEIGHT;
           if (I.kvh + 1 < Hkv) {
             ++I.kvh;
@@ -464,55 +490,63 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           hand_over();
         }
         const bool more = I.i1 >= 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pent[k] = ent[k];
+        pt0 = t0;
+        pseen = seen;
         if (more) {
-          const int t0 = I.span.tile(i) * PT_KEYS;
+          t0 = I.span.tile(i) * PT_KEYS;
+          seen = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int t = t0 + lane + 32 * k;
             const bool some = t < I.len && t >= I.first && ((t >= I.lo && t < I.hi) || t < I.pre);
-            tok[k] = some ? t : -1;
+            seen |= some ? 1u << k : 0u;
             ent[k] = some ? __ldg(C.page_table + (int64_t)I.b * C.max_pages + div_by(P.page, t)) : -1;
           }
-        }
-        if (x >= 0 && ok) load_tile(2 * x, x, &kmap, C.k);
-        const int e = (x + 1) & 1, v = (x + 1) % PT_VM;
-        if (more) {                                       // unit x + 1's offsets and token mask
-          uint32_t all = 0xffffffffu;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            int64_t o = -1;
-            if (tok[k] >= 0) {
-              if (ent[k] < 0 || ent[k] >= C.n_pages) paged_fail(C.status, ECHO_ERR_PAGE);
-              else o = (int64_t)ent[k] * C.page_stride +
-                       (int64_t)(tok[k] - div_by(P.page, tok[k]) * C.page_tokens) * C.row_stride;
-            }
-            S.row[e][lane + 32 * k] = o;
-            S.page[e][lane + 32 * k] = ent[k];
-            const uint32_t m = __ballot_sync(0xffffffffu, o >= 0);
-            all &= m;
-            if (lane == 0) S.vm[v][k] = m;
-          }
-          if (lane == 0) {
-            S.kvh[e] = I.kvh;
-            S.t0[e] = I.span.tile(i) * PT_KEYS;
-            S.whole[e] = all == 0xffffffffu;
-            pt_release(&S.vmtag[v], 2u * (uint32_t)(x + 2) + (all == 0xffffffffu ? 1u : 0u));
-          }
           ++i;
-        } else if (lane == 0) {
-          S.kvh[e] = -1;
         }
-        asm volatile("bar.sync 3, 64;" ::: "memory");     // warp 10 has unit x + 1
-        if (!more) break;
-        // after a failed wait the walk goes on without loads: warp 10 still meets its barriers
+        if (x > 0) {                                      // unit x - 1
+          const int e = (x - 1) % PT_UNITS, v = (x - 1) % PT_VM;
+          ok = ok && pt_wait(&S.uempty[e], (((x - 1) / PT_UNITS) & 1) ^ 1);
+          if (!ok) break;                                 // the others give up at their own waits
+          if (pkvh >= 0) {
+            uint32_t all = 0xffffffffu;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const bool page = pent[k] >= 0 && pent[k] < C.n_pages;
+              if (((pseen >> k) & 1u) && !page) paged_fail(C.status, ECHO_ERR_PAGE);
+              const uint32_t m = __ballot_sync(0xffffffffu, page);
+              all &= m;
+              if (lane == 0) S.vm[v][k] = m;
+              S.page[e][lane + 32 * k] = pent[k];
+            }
+            if (!box || all != 0xffffffffu) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int t = pt0 + lane + 32 * k;
+                const bool page = pent[k] >= 0 && pent[k] < C.n_pages;
+                S.row[e][lane + 32 * k] = page ? (int64_t)pent[k] * C.page_stride +
+                                                     (int64_t)(t - div_by(P.page, t) * C.page_tokens) * C.row_stride
+                                               : -1;
+              }
+            }
+            if (lane == 0) {
+              S.t0[e] = pt0;
+              S.whole[e] = box && all == 0xffffffffu;
+              pt_release(&S.vmtag[v], 2u * (uint32_t)x + (all == 0xffffffffu ? 1u : 0u));
+            }
+          }
+          __syncwarp();
+          if (lane == 0) {
+            S.kvh[e] = pkvh;
+            mbar_arrive(&S.ufull[e]);
+          }
+          if (pkvh < 0) break;
+        }
+        pkvh = more ? I.kvh : -1;
       }
     } else if (warp == 10) {
-      for (int x = 0;; ++x) {
-        asm volatile("bar.sync 3, 64;" ::: "memory");
-        if (S.kvh[x & 1] < 0) break;
-        if (ok) load_tile(2 * x + 1, x, &vmap, C.v);
-      }
-    } else if (warp == 11) {
       int nq[2] = {0, 0}, nitem = 0;
       while (ok) {
         const int e = nitem % PT_ITEMS;
@@ -556,12 +590,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       for (int h = 0; !ok && h < 2; ++h)
         if (nq[h]) pt_wait(&S.qfull[h], (nq[h] - 1) & 1);
     }
-    if (warp >= 9) {
-      cp_async_wait_all();
-      // after a failed wait, the copies in flight land before the CTA ends (bounded waits)
-      for (int g = max(0, issued - SLOTS); !ok && g < issued; ++g)
-        if ((g & 1) == (warp == 10 ? 1 : 0)) pt_wait(&S.full[g % SLOTS], (g / SLOTS) & 1);
-    }
+    if (warp == 10) cp_async_wait_all();
     if (warp == 8 && pt_elect()) {
     // ------------------------------------------------------------------ MMA --
       constexpr uint32_t id_qk = instr_desc(FMT_BF16, FMT_BF16, 0, 0, 128, 128);
@@ -640,6 +669,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           first = fresh;
         }
       }
+    }
     }
   } else {
     // -------------------------------------------------------------- softmax --

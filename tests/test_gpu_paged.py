@@ -320,6 +320,18 @@ def test_prefill_large_scores():
     _prefill([300], [300], 16, 4, 2, 128, BF, q_scale=30.0, seed=34)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_scales_of_zero_and_below(scale):
+    P = Paged([150], 16, 1, 64, BF, seed=36)
+    q = torch.randn(90, 3, 64, generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+    for cap in (0.0, 2.0):
+        out, lse = E.paged_attn_prefill(q, starts([90]), P.k, P.v, P.table, P.seq_len, scale, softcap=cap)
+        ref = attend(q.double().cpu(), P.K[0], P.V[0], range(60, 150), scale, dtype=BF, cap=cap)
+        check_rows("prompt", out, lse, ref)
+        out, lse = E.paged_attn_decode(q[-1:], P.k, P.v, P.table, P.seq_len, scale, softcap=cap)
+        check_rows("token", out, lse, tuple(x[-1:] for x in ref))
+
+
 def test_prefill_many_sequences():
     new = [i % 4 for i in range(300)]
     _prefill([n + (11 * i) % 40 for i, n in enumerate(new)], new, 8, 4, 2, 64, BF, seed=35)
