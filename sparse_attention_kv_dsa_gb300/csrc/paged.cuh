@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -92,9 +93,46 @@ inline ScoreForm score_form(const echo_attn_scores_t *s) {
   f.c = s->softcap * kPgLog2e;
   return f;
 }
+// 2^x, denormals as 0 (two units in the last place; half the cost of exp2f's full range).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float score_log2(const ScoreForm &f, float s) {
   const float y = s * f.a;
-  return f.capped ? f.c * (1.f - __fdividef(2.f, exp2f(y) + 1.f)) : y;
+  return f.capped ? f.c * (1.f - __fdividef(2.f, ex2(y) + 1.f)) : y;
+}
+
+// Allows kernel K its dynamic shared memory: once for each device, not with every launch (the
+// call costs several microseconds of host time).
+template <auto K>
+inline cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+// Launches K so that it may start up while the kernel before it in the stream ends; K itself
+// waits for it (griddepcontrol.wait) before it reads what that kernel wrote.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_after(void (*K)(KArgs...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, K, args...);
 }
 
 // The tiles of `tile` tokens that hold [first, pre) or [lo, hi): tiles tA .. tA + nA - 1, then

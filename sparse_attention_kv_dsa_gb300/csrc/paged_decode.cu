@@ -6,32 +6,42 @@
 // Bound: every seen key and value is read once (4 d bytes a token and KV head in bf16)
 // for 4 G d operations, G query heads to a KV head: 16 operations a byte at most, so HBM.
 //
-// Split.  The cache is dealt out in units: 64-token tiles (32 in float32) of one KV head and
-// up to 16 of its query heads, ordered by (sequence, KV head, tile).  A persistent grid
-// computes from the device's own lengths how many units there are and gives each CTA an equal
-// run of them, so that ragged batches, one long sequence and many short ones all spread
-// evenly, and one captured graph serves any lengths.  A run may cross sequences; the loads
-// run on across the border.  A (sequence, head) whose units lie in one CTA is finished
-// there; otherwise each of its CTAs leaves a partial (o, m, l) -- at most two a CTA: the end
-// of a run of units begun elsewhere (slot 0), and the start of one finished elsewhere (slot
-// 1) -- and a second kernel joins them in order: sums of a fixed order, no atomics.
+// Split.  The cache is dealt out in units: tiles of TILE tokens of one KV head and up to ROWS
+// of its query heads, ordered by (sequence, KV head, tile).  A persistent grid computes from
+// the device's own lengths how many units there are and gives each CTA an equal run of them,
+// so that ragged batches, one long sequence and many short ones all spread evenly, and one
+// captured graph serves any lengths.  A run may cross sequences; the loads run on across the
+// border.  A (sequence, head) whose units lie in one CTA is finished there; otherwise each of
+// its CTAs leaves a partial (o, m, l) -- at most two a CTA: the end of a run of units begun
+// elsewhere (slot 0), and the start of one finished elsewhere (slot 1) -- and a second kernel
+// joins them in order: sums of a fixed order, no atomics.
+//
+// Inside a CTA each warp takes its own share of every tile's tokens through its own ring of
+// cp.async stages with its own running maximum, so that the main loop has no barrier; the four
+// warps' states are joined where a (sequence, head) ends.
+// bf16: S = Q K^T and O += P V on the warp-level tensor instruction (16 query heads as its M;
+// G <= 16 leaves it idle rows, and still 16 operations a byte are an eighth of its rate).
+// float32: on the FMA units, exact products and sums: 8 tokens a warp, four lanes to a token
+// for the scores, a lane to four values for the results.
 
 #include "paged.cuh"
 
 namespace echo {
 
-constexpr int PD_THREADS = 128;
-constexpr int PD_ROWS = 16;          // query heads of a unit
+constexpr int PD_THREADS = 128, PD_WARPS = 4;
+constexpr int PD_MAX_ROWS = 16;
 constexpr int PD_MAX_CTAS = 608;     // partial slots: two a CTA
 constexpr int PD_MIN_UNITS = 2;      // fewest units of a CTA's run
 constexpr int PD_RING = 8;           // units whose look-ups are kept
+constexpr int PD_STAGES = 3;
 
 struct DecodeParams {
   echo_paged_kv_t C;
+  FastDiv page;                      // by page_tokens
   const void *q;
   int64_t q_stride;
   const int32_t *seq_len;
-  int B, Hq, G, HG;                  // query heads of a KV head, groups of 16 of them
+  int B, Hq, G, HG;                  // query heads of a KV head, groups of ROWS of them
   const float *slopes;
   int window;
   const int32_t *first_tok, *prefix_len;
@@ -39,11 +49,24 @@ struct DecodeParams {
   void *out;
   float *lse;
   float *po, *pml;                   // partials [2 CTAs][rows][d], [2 CTAs][rows][2]
-  int prows;                         // rows of a partial: min(G, 16)
+  int32_t *rec;                      // [CTAs][4]: the split (sequence, head group) that ends in the CTA
+  int prows;                         // rows of a partial: min(G, ROWS)
   int nctas;
 };
 
-// What sequence b's query sees, as tiles.
+template <typename T, int D>
+struct PdShape {
+  static constexpr bool BF = sizeof(T) == 2;
+  static constexpr int ROWS = BF ? 16 : 8;              // query heads of a unit
+  static constexpr int TW = BF ? (D == 128 ? 16 : 32) : 8;   // tokens of a warp: 8 KB of keys and values
+                                                        // (f32, d = 64: 4 KB)
+  static constexpr int TILE = PD_WARPS * TW;
+  static constexpr int ROWB = D * (int)sizeof(T);       // bytes of a key (or value)
+  static constexpr int HALF = TW * ROWB;                // a warp's keys of a tile
+};
+
+// What sequence b's query sees, as tiles; a sequence that sees nothing has one tile of
+// nothing, which writes its empty rows.
 struct DecodeSpan {
   int len, first, pre, lo;
   TileSpan t;
@@ -56,52 +79,34 @@ __device__ __forceinline__ DecodeSpan decode_span(const DecodeParams &P, int b, 
   s.pre = P.prefix_len ? min(P.prefix_len[b], s.len) : 0;
   s.lo = P.window ? max(s.first, s.len - P.window) : s.first;
   s.t = tile_span(s.first, s.pre, s.lo, s.len, tile);
+  if (s.n() == 0) s.t.nA = 1;
   return s;
 }
 
-// Sum over the block (every thread gets it).
-__device__ __forceinline__ long long block_sum(long long v, long long *warp) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) warp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  long long s = 0;
-#pragma unroll
-  for (int w = 0; w < PD_THREADS / 32; ++w) s += warp[w];
-  __syncthreads();
-  return s;
-}
-
-// Units of a CTA's run.
-__device__ __forceinline__ long long units_per_cta(long long total, int nctas) {
-  return max((total + nctas - 1) / nctas, (long long)PD_MIN_UNITS);
-}
-
-// A unit of the ring: its tile's rows, and what it is.
+// A unit of a warp's ring.
 struct UnitInfo {
-  int b, hh, t0, flags;              // flags: 1 first unit of the run for (b, hh), 2 last, 4 begun elsewhere, 8 goes on elsewhere
-  int len;
-};
-
-template <typename T, int TILE>
-struct PdShared {
-  int64_t row[PD_RING][TILE];        // offset of the token's row, -1: not seen
-  UnitInfo info[PD_RING];
-  long long warp[PD_THREADS / 32];
-  int seq;
-  long long before;
-  float mx[4][PD_ROWS], ls[4][PD_ROWS];
+  int b, hh, t0, len;                // t0: the warp's first token
+  int flags;                         // 1 the run's first unit of (b, hh), 2 its last, 4 begun elsewhere, 8 goes on elsewhere
+  uint32_t there;                    // tokens that are seen and there
 };
 
 template <typename T, int D>
-struct PdShape {
-  static constexpr int TILE = sizeof(T) == 2 ? 64 : 32;
-  static constexpr int STAGES = 3;
-  static constexpr int ROWB = D * (int)sizeof(T);       // bytes of a key (or value)
-  static constexpr int HALF = TILE * ROWB;              // bytes of a tile's keys
-  static constexpr int PBYTES = sizeof(T) == 2 ? PD_ROWS * TILE * 2 : PD_ROWS * TILE * 4;
-  static constexpr size_t SMEM = 128 + (size_t)STAGES * 2 * HALF + 2 * PD_ROWS * ROWB + PBYTES + sizeof(PdShared<T, TILE>);
+struct PdShared {
+  using Sh = PdShape<T, D>;
+  UnitInfo info[PD_WARPS][PD_RING];
+  long long sum[PD_WARPS];
+  int seq;
+  long long before;
+  float m[PD_WARPS][PD_MAX_ROWS], l[PD_WARPS][PD_MAX_ROWS];
+  alignas(16) float p[Sh::BF ? 1 : PD_WARPS][8][8];               // f32: weights [head][token]
 };
+
+template <typename T, int D>
+constexpr size_t pd_smem() {
+  using Sh = PdShape<T, D>;
+  return 128 + (size_t)PD_WARPS * PD_STAGES * 2 * Sh::HALF + Sh::ROWS * Sh::ROWB + Sh::ROWS * D * 4 +
+         sizeof(PdShared<T, D>);
+}
 
 __device__ __forceinline__ void pd_ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -123,6 +128,10 @@ __device__ __forceinline__ void pd_mma(float (&c)[4], const uint32_t (&a)[4], ui
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint32_t pd_pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
 
 // Byte offset of 16-byte chunk c of row r in a tile of ROWB-byte rows: chunks are permuted
 // within 128 bytes by the row, so that eight rows read at one chunk lie in eight bank groups.
@@ -131,107 +140,392 @@ __device__ __forceinline__ uint32_t pd_at(int r, int c) {
   return (uint32_t)(r * ROWB + ((c ^ (r & 7)) << 4));
 }
 
-template <typename T>
-__device__ __forceinline__ T pd_round(float x) {
-  if constexpr (sizeof(T) == 2) return __float2bfloat16_rn(x);
-  else return x;
-}
+// One warp's attention state in bf16: 16 heads x D values as tensor-instruction accumulators
+// (rows gid and gid + 8 of the lane).
+template <int D>
+struct WarpBf {
+  using T = __nv_bfloat16;
+  static constexpr int TW = PdShape<T, D>::TW, ROWB = PdShape<T, D>::ROWB;
+  float o[D / 8][4], m0, m1, l0, l1, sl0, sl1;
+  uint32_t qa[D / 16][4];
+
+  __device__ __forceinline__ void begin(const DecodeParams &P, const unsigned char *qt, int h0, int nrows, int lane) {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = sl0 = sl1 = 0.f;
+    const int gid = lane >> 2, mi = lane >> 3, r = (mi & 1) * 8 + (lane & 7);
+    if (P.slopes) {
+      if (gid < nrows) sl0 = P.slopes[h0 + gid] * kPgLog2e;
+      if (gid + 8 < nrows) sl1 = P.slopes[h0 + gid + 8] * kPgLog2e;
+    }
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) pd_ldsm_x4(smem_u32(qt) + pd_at<ROWB>(r, ks * 2 + (mi >> 1)), qa[ks]);
+  }
+
+  __device__ __forceinline__ void tile(const DecodeParams &P, const UnitInfo &I, const unsigned char *kt,
+                                       const unsigned char *vt, const unsigned char *, float (*)[8], int, int lane) {
+    const int mi = lane >> 3, tig = lane & 3;
+    float s[TW / 8][4];
+#pragma unroll
+    for (int i = 0; i < TW / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int g = 0; g < TW / 16; ++g) {
+        uint32_t b[4];
+        pd_ldsm_x4(smem_u32(kt) + pd_at<ROWB>(g * 16 + (mi >> 1) * 8 + (lane & 7), ks * 2 + (mi & 1)), b);
+        pd_mma(s[2 * g], qa[ks], b[0], b[1]);
+        pd_mma(s[2 * g + 1], qa[ks], b[2], b[3]);
+      }
+    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < TW / 8; ++t)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = t * 8 + 2 * tig + y;
+        float a = score_log2(P.f, s[t][y]), c = score_log2(P.f, s[t][2 + y]);
+        if (P.slopes) {
+          const float far = (float)(I.len - 1 - (I.t0 + r));
+          a -= sl0 * far;
+          c -= sl1 * far;
+        }
+        const bool ok = (I.there >> r) & 1u;
+        s[t][y] = ok ? a : -INFINITY;
+        s[t][2 + y] = ok ? c : -INFINITY;
+        mx0 = fmaxf(mx0, s[t][y]);
+        mx1 = fmaxf(mx1, s[t][2 + y]);
+      }
+#pragma unroll
+    for (int y = 1; y <= 2; y <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, y));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, y));
+    }
+    // a row's maximum moves a few times in a long sequence: the results are rescaled only then
+    if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
+      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+      const float c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), c1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= c0;
+      l1 *= c1;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= c0;
+        o[i][1] *= c0;
+        o[i][2] *= c1;
+        o[i][3] *= c1;
+      }
+    }
+    const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+    // weights, rounded to bf16 for the product (half a step, 2^-9 of each; the sums take the
+    // unrounded ones)
+#pragma unroll
+    for (int g = 0; g < TW / 16; ++g) {
+      uint32_t pa[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float *x = s[2 * g + t];
+        const float p0 = ex2(x[0] - z0), p1 = ex2(x[1] - z0), p2 = ex2(x[2] - z1), p3 = ex2(x[3] - z1);
+        l0 += p0 + p1;
+        l1 += p2 + p3;
+        pa[2 * t] = pd_pack(p0, p1);
+        pa[2 * t + 1] = pd_pack(p2, p3);
+      }
+      const int r = g * 16 + (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t b[4];
+        pd_ldsm_x4_t(smem_u32(vt) + pd_at<ROWB>(r, j * 2 + (mi >> 1)), b);
+        pd_mma(o[2 * j], pa, b[0], b[1]);
+        pd_mma(o[2 * j + 1], pa, b[2], b[3]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void stats(float *m, float *l, int, int lane) {
+    float s0 = l0, s1 = l1;
+#pragma unroll
+    for (int y = 1; y <= 2; y <<= 1) {
+      s0 += __shfl_xor_sync(0xffffffffu, s0, y);
+      s1 += __shfl_xor_sync(0xffffffffu, s1, y);
+    }
+    if ((lane & 3) == 0) {
+      m[lane >> 2] = m0;
+      m[(lane >> 2) + 8] = m1;
+      l[lane >> 2] = s0;
+      l[(lane >> 2) + 8] = s1;
+    }
+  }
+
+  // acc[row][value] (+)= f[row] * o
+  __device__ __forceinline__ void add_to(float *acc, const float *M, bool set, int, int lane) {
+    const int gid = lane >> 2, col = 2 * (lane & 3);
+    const float f0 = M[gid] == -INFINITY ? 0.f : ex2(m0 - M[gid]), f1 = M[gid + 8] == -INFINITY ? 0.f : ex2(m1 - M[gid + 8]);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      float2 *a = reinterpret_cast<float2 *>(acc + gid * D + i * 8 + col), *c = reinterpret_cast<float2 *>(acc + (gid + 8) * D + i * 8 + col);
+      float2 x = make_float2(o[i][0] * f0, o[i][1] * f0), y = make_float2(o[i][2] * f1, o[i][3] * f1);
+      if (!set) {
+        const float2 u = *a, v = *c;
+        x.x += u.x; x.y += u.y; y.x += v.x; y.y += v.y;
+      }
+      *a = x;
+      *c = y;
+    }
+  }
+};
+
+// One warp's attention state in float32: 8 heads, the lane's four values of each (d = 64: two
+// lanes share a chunk of values, each with half of the tokens).
+template <int D>
+struct WarpF32 {
+  static constexpr int KC = D / 4, ROWB = D * 4, LPC = 32 / KC;
+  float o[8][4], m[8], l[8], sl[8];
+
+  __device__ __forceinline__ void begin(const DecodeParams &P, const unsigned char *, int h0, int nrows, int) {
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      o[h][0] = o[h][1] = o[h][2] = o[h][3] = 0.f;
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+      sl[h] = P.slopes && h < nrows ? P.slopes[h0 + h] * kPgLog2e : 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void tile(const DecodeParams &P, const UnitInfo &I, const unsigned char *kt,
+                                       const unsigned char *vt, const unsigned char *qt, float (*pw)[8], int nrows, int lane) {
+    const int tk = lane >> 2, qd = lane & 3;              // token, and which of its four lanes
+    const bool ok = (I.there >> tk) & 1u;
+    const float far = (float)(I.len - 1 - (I.t0 + tk));
+    // the lane's chunks of its key: 4 (j ^ (tk & 1)) + qd, so that two rows differ in bank group
+    float4 kv[KC / 4];
+#pragma unroll
+    for (int j = 0; j < KC / 4; ++j)
+      kv[j] = *reinterpret_cast<const float4 *>(kt + pd_at<ROWB>(tk, 4 * (j ^ (tk & 1)) + qd));
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < nrows) {
+        const float4 *q = reinterpret_cast<const float4 *>(qt + h * ROWB) + qd;
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int j = 0; j < KC / 4; j += 2) {
+          const float4 x = q[4 * (j ^ (tk & 1))], y = q[4 * ((j + 1) ^ (tk & 1))];
+          a = fmaf(x.x, kv[j].x, fmaf(x.y, kv[j].y, fmaf(x.z, kv[j].z, fmaf(x.w, kv[j].w, a))));
+          b = fmaf(y.x, kv[j + 1].x, fmaf(y.y, kv[j + 1].y, fmaf(y.z, kv[j + 1].z, fmaf(y.w, kv[j + 1].w, b))));
+        }
+        float s = a + b;
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s = score_log2(P.f, s) - sl[h] * far;
+        s = ok ? s : -INFINITY;
+        float mx = s;
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+        if (mx > m[h]) {                                  // the same in every lane
+          const float c = ex2(m[h] - mx);
+          m[h] = mx;
+          l[h] *= c;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][e] *= c;
+        }
+        const float p = ex2(s - (m[h] == -INFINITY ? 0.f : m[h]));
+        l[h] += p;
+        if (qd == 0) pw[h][tk] = p;
+      }
+    __syncwarp();
+    const int c = lane % KC, part = lane / KC;
+    float4 vv[8 / LPC];
+#pragma unroll
+    for (int t = 0; t < 8 / LPC; ++t)
+      vv[t] = *reinterpret_cast<const float4 *>(vt + pd_at<ROWB>(part * (8 / LPC) + t, c));
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < nrows) {
+#pragma unroll
+        for (int t = 0; t < 8 / LPC; t += 4) {
+          const float4 p = *reinterpret_cast<const float4 *>(&pw[h][part * (8 / LPC) + t]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float w = u == 0 ? p.x : u == 1 ? p.y : u == 2 ? p.z : p.w;
+            o[h][0] = fmaf(w, vv[t + u].x, o[h][0]);
+            o[h][1] = fmaf(w, vv[t + u].y, o[h][1]);
+            o[h][2] = fmaf(w, vv[t + u].z, o[h][2]);
+            o[h][3] = fmaf(w, vv[t + u].w, o[h][3]);
+          }
+        }
+      }
+  }
+
+  __device__ __forceinline__ void stats(float *ms, float *ls, int nrows, int lane) {
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < nrows) {
+        float s = l[h];                                   // the four lanes of a token hold the same
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) s += __shfl_xor_sync(0xffffffffu, s, y);
+        if (lane == 0) {
+          ms[h] = m[h];
+          ls[h] = s;
+        }
+      }
+  }
+
+  __device__ __forceinline__ void add_to(float *acc, const float *M, bool set, int nrows, int lane) {
+    const int c = lane % KC;
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < nrows) {
+        const float f = M[h] == -INFINITY ? 0.f : ex2(m[h] - M[h]);
+        float4 x = make_float4(o[h][0] * f, o[h][1] * f, o[h][2] * f, o[h][3] * f);
+        if (LPC == 2) {
+          x.x += __shfl_xor_sync(0xffffffffu, x.x, 16);
+          x.y += __shfl_xor_sync(0xffffffffu, x.y, 16);
+          x.z += __shfl_xor_sync(0xffffffffu, x.z, 16);
+          x.w += __shfl_xor_sync(0xffffffffu, x.w, 16);
+        }
+        float4 *a = reinterpret_cast<float4 *>(acc + h * D) + c;
+        if (!set) {
+          const float4 u = *a;
+          x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
+        }
+        __syncwarp();                                     // d = 64: both lanes of a chunk have read it
+        *a = x;
+      }
+  }
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const __grid_constant__ DecodeParams P) {
   using Sh = PdShape<T, D>;
-  constexpr int TILE = Sh::TILE, ST = Sh::STAGES, ROWB = Sh::ROWB, HALF = Sh::HALF;
+  using State = std::conditional_t<Sh::BF, WarpBf<D>, WarpF32<D>>;
+  constexpr int TILE = Sh::TILE, TW = Sh::TW, ST = PD_STAGES, ROWB = Sh::ROWB, HALF = Sh::HALF, ROWS = Sh::ROWS;
   constexpr int KC = ROWB / 16;                          // 16-byte chunks of a key
-  constexpr bool BF = sizeof(T) == 2;
   extern __shared__ unsigned char pd_raw[];
   unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(pd_raw) + 127) & ~uintptr_t(127));
-  unsigned char *qs = sm + ST * 2 * HALF;                // two query tiles (this segment's and the next one's)
-  unsigned char *ps = qs + 2 * PD_ROWS * ROWB;           // probabilities of the tile
-  PdShared<T, TILE> &S = *reinterpret_cast<PdShared<T, TILE> *>(ps + Sh::PBYTES);
+  unsigned char *qs = sm + PD_WARPS * ST * 2 * HALF;     // the query tile
+  float *acc = reinterpret_cast<float *>(qs + ROWS * ROWB);                // the warps' results, joined
+  PdShared<T, D> &S = *reinterpret_cast<PdShared<T, D> *>(acc + ROWS * D);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const echo_paged_kv_t &C = P.C;
   const int HH = C.n_kv_heads * P.HG;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's run of units
-  long long mine = 0;
-  for (int b = tid; b < P.B; b += PD_THREADS) mine += decode_span(P, b, TILE).n();
-  const long long total = block_sum(mine, S.warp) * HH;
-  const long long per = units_per_cta(total, P.nctas);
-  const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
-  if (u0 >= u1) return;
-  // the sequence of unit u0: a scan over the sequences, PD_THREADS at a time
+  // ---- this CTA's run of units: a scan over the sequences, PD_THREADS at a time; with few
+  // sequences one scan gives the total and finds the place
+  long long total = 0, end = 0, n = 0;
   if (tid == 0) S.seq = -1;
-  long long base = 0;
   for (int b0 = 0; b0 < P.B; b0 += PD_THREADS) {
-    const int b = b0 + tid;
-    long long n = b < P.B ? (long long)decode_span(P, b, TILE).n() * HH : 0;
+    n = b0 + tid < P.B ? (long long)decode_span(P, b0 + tid, TILE).n() * HH : 0;
     long long x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) S.warp[warp] = x;
     __syncthreads();
-    long long pre = base;
-    for (int w = 0; w < warp; ++w) pre += S.warp[w];
-    const long long end = pre + x, start = end - n;
-    if (start <= u0 && u0 < end) { S.seq = b; S.before = start; }
-    for (int w = 0; w < PD_THREADS / 32; ++w) base += S.warp[w];
+    if (lane == 31) S.sum[warp] = x;
     __syncthreads();
-    if (S.seq >= 0) break;
+    end = total + x;
+#pragma unroll
+    for (int w = 0; w < PD_WARPS; ++w) {
+      if (w < warp) end += S.sum[w];
+      total += S.sum[w];
+    }
+  }
+  const long long per = max(total <= 0x7fffffff ? (long long)(((unsigned)total + P.nctas - 1) / (unsigned)P.nctas)
+                                                : (total + P.nctas - 1) / P.nctas, (long long)PD_MIN_UNITS);
+  const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
+  if (tid == 0) P.rec[blockIdx.x * 4] = 0;
+  if (u0 >= u1) return;
+  if (P.B <= PD_THREADS) {
+    if (end - n <= u0 && u0 < end) { S.seq = tid; S.before = end - n; }
+    __syncthreads();
+  } else {
+    long long base = 0;
+    for (int b0 = 0; b0 < P.B; b0 += PD_THREADS) {
+      n = b0 + tid < P.B ? (long long)decode_span(P, b0 + tid, TILE).n() * HH : 0;
+      long long x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) S.sum[warp] = x;
+      __syncthreads();
+      end = base + x;
+#pragma unroll
+      for (int w = 0; w < PD_WARPS; ++w) {
+        if (w < warp) end += S.sum[w];
+        base += S.sum[w];
+      }
+      if (end - n <= u0 && u0 < end) { S.seq = b0 + tid; S.before = end - n; }
+      __syncthreads();
+      if (S.seq >= 0) break;
+    }
   }
 
   // ---- cursor of the look-ups (the same in every thread)
-  int cb = S.seq, chh, ci;
+  int cb = S.seq;
   DecodeSpan cs = decode_span(P, cb, TILE);
+  int chh, ci;
   {
-    const long long off = u0 - S.before;
-    chh = (int)(off / cs.n());
-    ci = (int)(off % cs.n());
+    const long long off = u0 - S.before;                 // below 2^31 tiles times heads of one sequence
+    const int cn = cs.n();
+    chh = off <= 0x7fffffff ? (int)((unsigned)off / (unsigned)cn) : (int)(off / cn);
+    ci = (int)(off - (long long)chh * cn);
   }
-  const int nu = (int)(u1 - u0);                         // a run is at most 2^31 tokens of one head ... in tiles
+  const int c0 = (int)((u0 - ci) / per);                 // CTA in which the first (sequence, head group) begins
+  const int nu = (int)(u1 - u0);
   int cu = 0;                                            // units looked up
-  // look up unit cu: thread r < TILE finds its token's row
+  int32_t ent = -1;                                      // the last one's page-table entry of this lane's token
+  int tok = -1;
+  UnitInfo *ring = S.info[warp];
   auto look_up = [&]() {
+    tok = -1;
     if (cu >= nu) return;
-    const int e = cu % PD_RING;
-    const int t0 = cs.t.tile(ci) * TILE;
-    if (tid < TILE) {
-      const int t = t0 + tid;
-      const bool seen = t >= cs.first && t < cs.len && (t >= cs.lo || t < cs.pre);
-      S.row[e][tid] = seen ? paged_row(C, cb, t) : -1;
+    const int cn = cs.n(), t0 = cs.t.tile(ci) * TILE + warp * TW;
+    const int t = t0 + lane;
+    if (lane < TW && t >= cs.first && t < cs.len && (t >= cs.lo || t < cs.pre)) {
+      tok = t;
+      ent = __ldg(C.page_table + (int64_t)cb * C.max_pages + div_by(P.page, t));
     }
-    if (tid == PD_THREADS - 1) {
-      UnitInfo I;
+    if (lane == 0) {
+      UnitInfo &I = ring[cu % PD_RING];
+      const bool last = ci + 1 == cn || cu + 1 == nu;
       I.b = cb; I.hh = chh; I.t0 = t0; I.len = cs.len;
-      const bool lastu = ci + 1 == cs.n() || cu + 1 == nu;
-      I.flags = ((ci == 0 || cu == 0) ? 1 : 0) | (lastu ? 2 : 0) | ((cu < ci) ? 4 : 0) |
-                ((lastu && ci + 1 != cs.n()) ? 8 : 0);
-      S.info[e] = I;
+      I.flags = ((ci == 0 || cu == 0) ? 1 : 0) | (last ? 2 : 0) | (cu < ci ? 4 : 0) | (last && ci + 1 != cn ? 8 : 0);
     }
     ++cu;
-    if (++ci == cs.n()) {
+    if (++ci == cn) {
       ci = 0;
       if (++chh == HH) {
         chh = 0;
-        if (cu < nu) {
-          do cs = decode_span(P, ++cb, TILE); while (cs.n() == 0 && cb < P.B - 1);
-        }
+        if (cu < nu && cb + 1 < P.B) cs = decode_span(P, ++cb, TILE);
       }
     }
   };
-  // copy unit x's keys and values into its stage
+  // turns unit x's entries into offsets and copies the warp's keys and values into its stage
+  unsigned char *stages = sm + warp * ST * 2 * HALF;
   auto load = [&](int x) {
     if (x < nu) {
-      const int e = x % PD_RING;
-      const int kvh = S.info[e].hh / P.HG;
-      const T *kb = (const T *)C.k + (int64_t)kvh * C.head_stride, *vb = (const T *)C.v + (int64_t)kvh * C.head_stride;
-      unsigned char *kt = sm + (x % ST) * 2 * HALF, *vt = kt + HALF;
-#pragma unroll 4
-      for (int i = tid; i < TILE * KC; i += PD_THREADS) {
-        const int r = i / KC, c = i % KC;
-        const int64_t g = S.row[e][r];
+      int64_t row = -1;
+      if (tok >= 0) {
+        if (ent < 0 || ent >= C.n_pages) paged_fail(C.status, ECHO_ERR_PAGE);
+        else row = (int64_t)ent * C.page_stride + (int64_t)(tok - div_by(P.page, tok) * C.page_tokens) * C.row_stride;
+      }
+      const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
+      UnitInfo &I = ring[x % PD_RING];
+      if (lane == 0) I.there = there;
+      __syncwarp();
+      const int64_t head = (int64_t)(I.hh / P.HG) * C.head_stride;
+      const T *kb = (const T *)C.k + head, *vb = (const T *)C.v + head;
+      unsigned char *kt = stages + (x % ST) * 2 * HALF, *vt = kt + HALF;
+#pragma unroll
+      for (int i = 0; i < TW * KC / 32; ++i) {
+        const int r = (i * 32 + lane) / KC, c = (i * 32 + lane) % KC;
+        const int64_t g = __shfl_sync(0xffffffffu, row, r);
         const int64_t off = (g >= 0 ? g : 0) + c * (16 / (int)sizeof(T));
         const uint32_t nbytes = g >= 0 ? 16u : 0u;
         cp_async_16(kt + pd_at<ROWB>(r, c), kb + off, nbytes);
@@ -240,335 +534,146 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const __grid_c
     }
     cp_async_commit();
   };
-  for (int i = 0; i < ST; ++i) look_up();
-  __syncthreads();
-  for (int i = 0; i < ST - 1; ++i) load(i);
+  for (int i = 0; i < ST - 1; ++i) {
+    look_up();
+    load(i);
+  }
+  look_up();
 
-  float o[BF ? D / 32 : 4][4];                           // bf16: n-tiles of D/4 values; f32: heads x 4 values
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;      // bf16: rows gid, gid + 8
-  float mh[4], lh[4];                                    // f32: this warp's heads
-  uint32_t qa[BF ? D / 16 : 1][4];
-  const int gid = lane >> 2, tig = lane & 3;
-  float sl0 = 0.f, sl1 = 0.f, slh[4] = {0.f, 0.f, 0.f, 0.f};
-  int nrows = 0, h0 = 0, nseg = 0;
-
+  State A;
+  int nrows = 0, h0 = 0;
   for (int x = 0; x < nu; ++x) {
-    const int e = x % PD_RING;
-    const UnitInfo I = S.info[e];
-    if (I.flags & 1) {                                   // a new (sequence, head group)
-      const int kvh = I.hh / P.HG, hg = I.hh % P.HG;
-      h0 = kvh * P.G + hg * PD_ROWS;
-      nrows = min(PD_ROWS, P.G - hg * PD_ROWS);
-      unsigned char *qt = qs + (nseg & 1) * PD_ROWS * ROWB;
-      ++nseg;
+    cp_async_wait<ST - 2>();
+    __syncwarp();                                        // unit x is there, and unit x - 1's stage is free
+    load(x + ST - 1);
+    look_up();                                           // unit x + ST
+    const UnitInfo &I = ring[x % PD_RING];
+    if (I.flags & 1) {                                   // a new (sequence, head group): every warp is past the last one
+      const int hg = I.hh % P.HG;
+      h0 = (I.hh / P.HG) * P.G + hg * ROWS;
+      nrows = min(ROWS, P.G - hg * ROWS);
       const T *q = (const T *)P.q + (int64_t)I.b * P.q_stride + (int64_t)h0 * D;
-      for (int i = tid; i < PD_ROWS * KC; i += PD_THREADS) {
+      for (int i = tid; i < ROWS * KC; i += PD_THREADS) {
         const int r = i / KC, c = i % KC;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (r < nrows) v = reinterpret_cast<const uint4 *>(q + (int64_t)r * D)[c];
-        *reinterpret_cast<uint4 *>(qt + pd_at<ROWB>(r, c)) = v;
+        *reinterpret_cast<uint4 *>(qs + (Sh::BF ? pd_at<ROWB>(r, c) : r * ROWB + c * 16)) = v;
       }
-#pragma unroll
-      for (int i = 0; i < (BF ? D / 32 : 4); ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      m0 = m1 = -INFINITY;
-      l0 = l1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { mh[i] = -INFINITY; lh[i] = 0.f; }
-      if (P.slopes) {
-        if constexpr (BF) {
-          sl0 = gid < nrows ? P.slopes[h0 + gid] * kPgLog2e : 0.f;
-          sl1 = gid + 8 < nrows ? P.slopes[h0 + gid + 8] * kPgLog2e : 0.f;
-        } else {
-          for (int i = 0; i < 4; ++i) slh[i] = warp + 4 * i < nrows ? P.slopes[h0 + warp + 4 * i] * kPgLog2e : 0.f;
-        }
-      }
+      __syncthreads();
+      A.begin(P, qs, h0, nrows, lane);
     }
-    look_up();                                           // unit x + ST
-    cp_async_wait<ST - 2>();
-    __syncthreads();                                     // unit x is there; unit x - 1's stage is free
-    load(x + ST - 1);
-    const unsigned char *kt = sm + (x % ST) * 2 * HALF, *vt = kt + HALF;
-    const unsigned char *qt = qs + ((nseg - 1) & 1) * PD_ROWS * ROWB;
-
-    if constexpr (BF) {
-      if (I.flags & 1) {
-        const int mi = lane >> 3, r = (mi & 1) * 8 + (lane & 7);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) pd_ldsm_x4(smem_u32(qt) + pd_at<ROWB>(r, ks * 2 + (mi >> 1)), qa[ks]);
-      }
-      // scores of this warp's 16 tokens
-      const int rw = warp * 16;
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      {
-        const int mi = lane >> 3, r = rw + (mi >> 1) * 8 + (lane & 7);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t b[4];
-          pd_ldsm_x4(smem_u32(kt) + pd_at<ROWB>(r, ks * 2 + (mi & 1)), b);
-          pd_mma(s[0], qa[ks], b[0], b[1]);
-          pd_mma(s[1], qa[ks], b[2], b[3]);
-        }
-      }
-      float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int r = rw + t * 8 + 2 * tig + y;
-          const bool ok = S.row[e][r] >= 0;
-          float a = score_log2(P.f, s[t][y]), c = score_log2(P.f, s[t][2 + y]);
-          if (P.slopes) {
-            const float far = (float)(I.len - 1 - (I.t0 + r));
-            a -= sl0 * far;
-            c -= sl1 * far;
-          }
-          s[t][y] = ok ? a : -INFINITY;
-          s[t][2 + y] = ok ? c : -INFINITY;
-          mx0 = fmaxf(mx0, s[t][y]);
-          mx1 = fmaxf(mx1, s[t][2 + y]);
-        }
-#pragma unroll
-      for (int y = 1; y <= 2; y <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, y));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, y));
-      }
-      if (tig == 0) {
-        S.mx[warp][gid] = mx0;
-        S.mx[warp][gid + 8] = mx1;
-      }
+    const unsigned char *kt = stages + (x % ST) * 2 * HALF;
+    A.tile(P, I, kt, kt + HALF, qs, S.p[Sh::BF ? 0 : warp], nrows, lane);
+    if (I.flags & 2) {                                   // the run's last unit of this (sequence, head group)
+      A.stats(S.m[warp], S.l[warp], nrows, lane);
       __syncthreads();
+      float *M = S.m[0];
+      if (warp == 0 && lane < nrows) {                   // joined: (m, l) of warp 0's entries
+        float mm = S.m[0][lane], ll = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        mx0 = fmaxf(mx0, S.mx[w][gid]);
-        mx1 = fmaxf(mx1, S.mx[w][gid + 8]);
+        for (int w = 1; w < PD_WARPS; ++w) mm = fmaxf(mm, S.m[w][lane]);
+#pragma unroll
+        for (int w = 0; w < PD_WARPS; ++w) ll += mm == -INFINITY ? 0.f : ex2(S.m[w][lane] - mm) * S.l[w][lane];
+        S.m[0][lane] = mm;
+        S.l[0][lane] = ll;
       }
-      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-      const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
-      const float c0 = exp2f(m0 - z0), c1 = exp2f(m1 - z1);
-      m0 = n0;
-      m1 = n1;
-      // probabilities in bf16 (half a step, 2^-9 of each; the sums take the unrounded ones)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float p0 = exp2f(s[t][0] - z0), p1 = exp2f(s[t][1] - z0), p2 = exp2f(s[t][2] - z1), p3 = exp2f(s[t][3] - z1);
-        if (t == 0) { l0 *= c0; l1 *= c1; }
-        l0 += p0 + p1;
-        l1 += p2 + p3;
-        const int ch = (rw + t * 8) / 8;
-        const __nv_bfloat162 a = __floats2bfloat162_rn(p0, p1), c = __floats2bfloat162_rn(p2, p3);
-        *reinterpret_cast<__nv_bfloat162 *>(ps + pd_at<TILE * 2>(gid, ch) + 4 * tig) = a;
-        *reinterpret_cast<__nv_bfloat162 *>(ps + pd_at<TILE * 2>(gid + 8, ch) + 4 * tig) = c;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        o[i][0] *= c0;
-        o[i][1] *= c0;
-        o[i][2] *= c1;
-        o[i][3] *= c1;
-      }
-      // o[:, this warp's D/4 values] += P (16 x 64) V
-      {
-        const int mi = lane >> 3;
-#pragma unroll
-        for (int ks = 0; ks < TILE / 16; ++ks) {
-          uint32_t a[4];
-          pd_ldsm_x4(smem_u32(ps) + pd_at<TILE * 2>((mi & 1) * 8 + (lane & 7), ks * 2 + (mi >> 1)), a);
-          const int r = ks * 16 + (mi & 1) * 8 + (lane & 7);
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            uint32_t b[4];
-            pd_ldsm_x4_t(smem_u32(vt) + pd_at<ROWB>(r, warp * (D / 32) + j * 2 + (mi >> 1)), b);
-            pd_mma(o[2 * j], a, b[0], b[1]);
-            pd_mma(o[2 * j + 1], a, b[2], b[3]);
-          }
-        }
-      }
-      if (I.flags & 2) {                                 // the run's last unit of this (sequence, head group)
-        float s0 = l0, s1 = l1;
-#pragma unroll
-        for (int y = 1; y <= 2; y <<= 1) {
-          s0 += __shfl_xor_sync(0xffffffffu, s0, y);
-          s1 += __shfl_xor_sync(0xffffffffu, s1, y);
-        }
-        if (tig == 0) {
-          S.ls[warp][gid] = s0;
-          S.ls[warp][gid + 8] = s1;
-        }
+      for (int w = 0; w < PD_WARPS; ++w) {
         __syncthreads();
-        const float L0 = S.ls[0][gid] + S.ls[1][gid] + S.ls[2][gid] + S.ls[3][gid];
-        const float L1 = S.ls[0][gid + 8] + S.ls[1][gid + 8] + S.ls[2][gid + 8] + S.ls[3][gid + 8];
-        const bool whole = !(I.flags & 12);
-        const int slot = 2 * blockIdx.x + ((I.flags & 4) ? 0 : 1);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = gid + 8 * half;
-          if (r >= nrows) continue;
-          const float L = half ? L1 : L0, M = half ? m1 : m0;
-          if (whole) {
-            const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-            T *dst = (T *)P.out + ((int64_t)I.b * P.Hq + h0 + r) * D + warp * (D / 4) + 2 * tig;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              *reinterpret_cast<__nv_bfloat162 *>(dst + 8 * i) =
-                  __floats2bfloat162_rn(o[i][2 * half] * inv, o[i][2 * half + 1] * inv);
-            if (warp == 0 && tig == 0)
-              P.lse[(int64_t)I.b * P.Hq + h0 + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPgLn2;
-          } else {
-            float *dst = P.po + ((int64_t)slot * P.prows + r) * D + warp * (D / 4) + 2 * tig;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              *reinterpret_cast<float2 *>(dst + 8 * i) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
-            if (warp == 0 && tig == 0)
-              *reinterpret_cast<float2 *>(P.pml + ((int64_t)slot * P.prows + r) * 2) = make_float2(M, L);
-          }
+        if (warp == w) A.add_to(acc, M, w == 0, nrows, lane);
+      }
+      __syncthreads();
+      const bool whole = !(I.flags & 12);
+      const int64_t slot = 2 * blockIdx.x + ((I.flags & 4) ? 0 : 1);
+      for (int i = tid; i < nrows * (D / 4); i += PD_THREADS) {
+        const int r = i / (D / 4), c = i % (D / 4);
+        float4 v = *reinterpret_cast<const float4 *>(acc + r * D + 4 * c);
+        if (whole) {
+          const float L = S.l[0][r], inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+          v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+          T *dst = (T *)P.out + ((int64_t)I.b * P.Hq + h0 + r) * D + 4 * c;
+          if constexpr (Sh::BF) *reinterpret_cast<uint2 *>(dst) = make_uint2(pd_pack(v.x, v.y), pd_pack(v.z, v.w));
+          else *reinterpret_cast<float4 *>(dst) = v;
+        } else {
+          *reinterpret_cast<float4 *>(P.po + (slot * P.prows + r) * D + 4 * c) = v;
         }
       }
-    } else {
-      // float32: warp w takes heads w, w + 4, ...; lane = token for the scores, then lane = a
-      // 16-byte chunk of the values (D = 64: two lanes' halves of the tokens for each chunk)
-      const float *pt = reinterpret_cast<const float *>(ps);
-      const bool ok = S.row[e][lane] >= 0;
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      const int nh = (nrows - warp + 3) / 4;             // heads of this warp
-      if (nh > 0) {
-        for (int c = 0; c < KC; ++c) {
-          const float4 kv = *reinterpret_cast<const float4 *>(kt + pd_at<ROWB>(lane, c));
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < nh) {
-              const int r = warp + 4 * i;
-              const float4 qv = *reinterpret_cast<const float4 *>(qt + pd_at<ROWB>(r, c));
-              s[i] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[i]))));
-            }
-        }
-        const float far = (float)(I.len - 1 - (I.t0 + lane));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < nh) {
-            float a = score_log2(P.f, s[i]);
-            if (P.slopes) a -= slh[i] * far;
-            a = ok ? a : -INFINITY;
-            float mx = a;
-#pragma unroll
-            for (int y = 16; y > 0; y >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
-            const float nm = fmaxf(mh[i], mx), z = nm == -INFINITY ? 0.f : nm;
-            const float c = exp2f(mh[i] - z), p = exp2f(a - z);
-            mh[i] = nm;
-            lh[i] = lh[i] * c + p;
-            reinterpret_cast<float *>(ps)[(warp + 4 * i) * TILE + lane] = p;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] *= c;
-          }
-        __syncwarp();
-        constexpr int LPT = 32 / KC;                     // lanes of a chunk: 1 (D = 128) or 2
-        const int c = lane % KC, part = lane / KC;
-        for (int r = part; r < TILE; r += LPT) {
-          const float4 vv = *reinterpret_cast<const float4 *>(vt + pd_at<ROWB>(r, c));
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < nh) {
-              const float p = pt[(warp + 4 * i) * TILE + r];
-              o[i][0] = fmaf(p, vv.x, o[i][0]);
-              o[i][1] = fmaf(p, vv.y, o[i][1]);
-              o[i][2] = fmaf(p, vv.z, o[i][2]);
-              o[i][3] = fmaf(p, vv.w, o[i][3]);
-            }
-        }
-        if (I.flags & 2) {
-          const bool whole = !(I.flags & 12);
-          const int slot = 2 * blockIdx.x + ((I.flags & 4) ? 0 : 1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < nh) {
-              float L = lh[i];
-#pragma unroll
-              for (int y = 16; y > 0; y >>= 1) L += __shfl_xor_sync(0xffffffffu, L, y);
-              float4 v = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-              if (LPT == 2) {
-                v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
-                v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
-                v.z += __shfl_xor_sync(0xffffffffu, v.z, 16);
-                v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
-              }
-              const int r = warp + 4 * i;
-              if (whole) {
-                const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-                if (part == 0)
-                  *reinterpret_cast<float4 *>((float *)P.out + ((int64_t)I.b * P.Hq + h0 + r) * D + 4 * c) =
-                      make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                if (lane == 0)
-                  P.lse[(int64_t)I.b * P.Hq + h0 + r] = L == 0.f ? -INFINITY : (mh[i] + log2f(L)) * kPgLn2;
-              } else {
-                if (part == 0) *reinterpret_cast<float4 *>(P.po + ((int64_t)slot * P.prows + r) * D + 4 * c) = v;
-                if (lane == 0)
-                  *reinterpret_cast<float2 *>(P.pml + ((int64_t)slot * P.prows + r) * 2) = make_float2(mh[i], L);
-              }
-            }
-        }
+      if (tid < nrows) {
+        const float mm = S.m[0][tid], L = S.l[0][tid];
+        if (whole) P.lse[(int64_t)I.b * P.Hq + h0 + tid] = L == 0.f ? -INFINITY : (mm + log2f(L)) * kPgLn2;
+        else *reinterpret_cast<float2 *>(P.pml + (slot * P.prows + tid) * 2) = make_float2(mm, L);
+      }
+      if (tid == 0 && (I.flags & 12) == 4) {             // a split one ends here: to be joined
+        int32_t *rec = P.rec + blockIdx.x * 4;
+        rec[1] = c0;
+        rec[2] = I.b;
+        rec[3] = I.hh;
+        rec[0] = 1;
       }
     }
   }
   cp_async_wait_all();
 }
 
-// Joins the partials of one (sequence, head group) in the order of their units, and gives a
-// sequence that sees nothing its empty rows.  One CTA each; a warp takes every fourth row.
+// Joins the partials of the (sequence, head group) that ends in CTA blockIdx.x: slot 1 of its
+// first CTA, then slot 0 of the following ones.  A block takes one row, a thread one value; the
+// maxima first, then the weighted sums in the order of the CTAs.
 template <typename T, int D>
-__global__ void __launch_bounds__(PD_THREADS) paged_decode_join_kernel(const __grid_constant__ DecodeParams P) {
-  constexpr int TILE = PdShape<T, D>::TILE, VL = D / 32;
-  __shared__ long long warp_sum[PD_THREADS / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int HH = P.C.n_kv_heads * P.HG, b = blockIdx.x / HH, hh = blockIdx.x % HH;
-  long long all = 0, before = 0;
-  int n = 0;
-  for (int i = tid; i < P.B; i += PD_THREADS) {
-    const int k = decode_span(P, i, TILE).n();
-    all += k;
-    if (i < b) before += k;
+__global__ void __launch_bounds__(D) paged_decode_join_kernel(const __grid_constant__ DecodeParams P) {
+  __shared__ float wt[PD_MAX_CTAS];
+  __shared__ float red[2][D / 32];
+  constexpr int ROWS = PdShape<T, D>::ROWS;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c1 = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
+  const int4 rec = *reinterpret_cast<const int4 *>(P.rec + c1 * 4);
+  if (rec.x == 0) return;
+  const int c0 = rec.y, b = rec.z, hh = rec.w, hg = hh % P.HG;
+  if (r >= min(ROWS, P.G - hg * ROWS)) return;
+  const int np = c1 - c0 + 1;
+  auto row = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * P.prows + r; };
+  float M = -INFINITY;
+  for (int i = tid; i < np; i += D) M = fmaxf(M, P.pml[row(i) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if ((tid & 31) == 0) red[0][tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) M = fmaxf(M, red[0][w]);
+  float L = 0.f;
+  for (int i = tid; i < np; i += D) {
+    const float2 ml = *reinterpret_cast<const float2 *>(P.pml + row(i) * 2);
+    const float w = M == -INFINITY ? 0.f : ex2(ml.x - M);
+    wt[i] = w;
+    L += w * ml.y;
   }
-  n = decode_span(P, b, TILE).n();
-  const long long per = units_per_cta(block_sum(all, warp_sum) * HH, P.nctas);
-  const long long s0 = block_sum(before, warp_sum) * HH + (long long)hh * n, s1 = s0 + n;
-  const int hg = hh % P.HG, h0 = (hh / P.HG) * P.G + hg * PD_ROWS, nrows = min(PD_ROWS, P.G - hg * PD_ROWS);
-  const long long c0 = n ? s0 / per : 0, c1 = n ? (s1 - 1) / per : 0;
-  if (n && c0 == c1) return;                             // finished by its CTA
-  for (int r = warp; r < nrows; r += PD_THREADS / 32) {
-    float M = -INFINITY, L = 0.f, v[VL];
 #pragma unroll
-    for (int i = 0; i < VL; ++i) v[i] = 0.f;
-    if (n) {
-      for (long long c = c0; c <= c1; ++c) {
-        const int64_t row = (2 * c + (c == c0 ? 1 : 0)) * P.prows + r;
-        const float m = P.pml[row * 2], l = P.pml[row * 2 + 1];
-        const float nm = fmaxf(M, m), z = nm == -INFINITY ? 0.f : nm;
-        const float wa = exp2f(M - z), wb = exp2f(m - z);
-        M = nm;
-        L = L * wa + l * wb;
-        const float *o = P.po + row * D + lane * VL;
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if ((tid & 31) == 0) red[1][tid >> 5] = L;
+  __syncthreads();
+  L = 0.f;
 #pragma unroll
-        for (int i = 0; i < VL; ++i) v[i] = v[i] * wa + o[i] * wb;
-      }
-    }
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    T *dst = (T *)P.out + ((int64_t)b * P.Hq + h0 + r) * D + lane * VL;
-#pragma unroll
-    for (int i = 0; i < VL; ++i) dst[i] = pd_round<T>(v[i] * inv);
-    if (lane == 0) P.lse[(int64_t)b * P.Hq + h0 + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPgLn2;
-  }
+  for (int w = 0; w < D / 32; ++w) L += red[1][w];
+  float v = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < np; ++i) v = fmaf(wt[i], P.po[row(i) * D + tid], v);
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+  const int64_t orow = (int64_t)b * P.Hq + (hh / P.HG) * P.G + hg * ROWS + r;
+  if constexpr (sizeof(T) == 2) ((T *)P.out)[orow * D + tid] = __float2bfloat16_rn(v * inv);
+  else ((T *)P.out)[orow * D + tid] = v * inv;
+  if (tid == 0) P.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPgLn2;
 }
 
 template <typename T, int D>
 static echo_status_t launch_decode(DecodeParams &P, cudaStream_t st) {
-  using Sh = PdShape<T, D>;
-  static_assert(Sh::SMEM <= 227 * 1024, "fits an SM");
-  constexpr int occ = (int)std::min<size_t>(4, 227 * 1024 / (Sh::SMEM + 1024));
+  constexpr size_t smem = pd_smem<T, D>();
+  constexpr int occ = (int)std::min<size_t>(4, 227 * 1024 / (smem + 1024));
+  static_assert(occ >= 2, "two CTAs an SM hide one another's latencies");
+  P.HG = (P.G + PdShape<T, D>::ROWS - 1) / PdShape<T, D>::ROWS;
+  P.prows = std::min(P.G, PdShape<T, D>::ROWS);
   P.nctas = std::min(sm_count() * occ, PD_MAX_CTAS);
-  ECHO_CUDA_OK(cudaFuncSetAttribute(paged_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::SMEM));
-  paged_decode_kernel<T, D><<<P.nctas, PD_THREADS, Sh::SMEM, st>>>(P);
+  ECHO_CUDA_OK((allow_smem<paged_decode_kernel<T, D>>(smem)));
+  paged_decode_kernel<T, D><<<P.nctas, PD_THREADS, smem, st>>>(P);
   ECHO_LAUNCH_OK();
-  paged_decode_join_kernel<T, D><<<P.B * P.C.n_kv_heads * P.HG, PD_THREADS, 0, st>>>(P);
-  ECHO_LAUNCH_OK();
+  ECHO_CUDA_OK(launch_after(paged_decode_join_kernel<T, D>, dim3(P.nctas, P.prows), dim3(D), st, P));
   return ECHO_OK;
 }
 
@@ -578,7 +683,7 @@ using namespace echo;
 
 extern "C" size_t echo_paged_decode_workspace_bytes(int32_t Hq, int32_t n_kv_heads, int32_t d) {
   if (Hq <= 0 || n_kv_heads <= 0 || d <= 0 || Hq % n_kv_heads) return 0;
-  return (size_t)2 * PD_MAX_CTAS * std::min(Hq / n_kv_heads, PD_ROWS) * (d + 2) * sizeof(float);
+  return (size_t)PD_MAX_CTAS * (2 * std::min(Hq / n_kv_heads, PD_MAX_ROWS) * (d + 2) + 4) * sizeof(float);
 }
 
 extern "C" echo_status_t echo_paged_attn_decode(const echo_paged_kv_t *cache, const void *q, int64_t q_stride,
@@ -598,16 +703,16 @@ extern "C" echo_status_t echo_paged_attn_decode(const echo_paged_kv_t *cache, co
     return ECHO_ERR_INVALID_ARG;
   DecodeParams P;
   P.C = *cache;
+  P.page = fast_div(cache->page_tokens);
   P.q = q; P.q_stride = q_stride; P.seq_len = seq_len;
-  P.B = B; P.Hq = Hq; P.G = Hq / cache->n_kv_heads; P.HG = (P.G + PD_ROWS - 1) / PD_ROWS;
-  if ((int64_t)B * cache->n_kv_heads * P.HG > 0x7fffffff) return ECHO_ERR_UNSUPPORTED;
+  P.B = B; P.Hq = Hq; P.G = Hq / cache->n_kv_heads;
   P.slopes = scores->slopes; P.window = scores->window;
   P.first_tok = scores->first_tok; P.prefix_len = scores->prefix_len;
   P.f = score_form(scores);
   P.out = out; P.lse = lse;
-  P.prows = std::min(P.G, PD_ROWS);
-  P.po = reinterpret_cast<float *>(workspace);
-  P.pml = P.po + (size_t)2 * PD_MAX_CTAS * P.prows * cache->head_dim;
+  P.rec = reinterpret_cast<int32_t *>(workspace);
+  P.po = reinterpret_cast<float *>(P.rec + 4 * PD_MAX_CTAS);
+  P.pml = P.po + (size_t)2 * PD_MAX_CTAS * std::min(P.G, PD_MAX_ROWS) * cache->head_dim;
   cudaStream_t cs = (cudaStream_t)stream;
   if (cache->dtype == ECHO_BF16)
     return cache->head_dim == 128 ? launch_decode<__nv_bfloat16, 128>(P, cs) : launch_decode<__nv_bfloat16, 64>(P, cs);

@@ -237,8 +237,7 @@ template <int D>
 static echo_status_t launch_simt(const PrefillParams &P, cudaStream_t st) {
   const int64_t tiles = ((int64_t)P.N * P.G + PS_ROWS - 1) / PS_ROWS + P.B;
   if (tiles > 0x7fffffff) return ECHO_ERR_UNSUPPORTED;
-  ECHO_CUDA_OK(cudaFuncSetAttribute(paged_prefill_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)ps_smem<D>()));
+  ECHO_CUDA_OK(allow_smem<paged_prefill_simt_kernel<D>>(ps_smem<D>()));
   paged_prefill_simt_kernel<D><<<dim3((unsigned)tiles, P.C.n_kv_heads), PS_THREADS, ps_smem<D>(), st>>>(P);
   ECHO_LAUNCH_OK();
   return ECHO_OK;

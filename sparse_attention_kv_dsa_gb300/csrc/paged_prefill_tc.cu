@@ -113,11 +113,6 @@ __device__ __forceinline__ void pt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ float pt_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // One lane of the warp.  The compiler knows the branch for a single thread's: its TMA and MMA
 // instructions take their operands straight from uniform registers, where `lane == 0` made it
 // write a loop over the active lanes around each (an issue took some 100 cycles).
@@ -767,7 +762,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           if (i == i0) {
             m = mx;
           } else if (__any_sync(0xffffffffu, nm != m)) {
-            const float corr = nm != m ? pt_ex2(m - nm) : 1.f;
+            const float corr = nm != m ? ex2(m - nm) : 1.f;
             m = nm;
             l *= corr;
             if (!pt_wait(&S.pvdone[t], (ns - 1) & 1)) { ok = false; break; }
@@ -794,8 +789,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
             for (int q = 0; q < 32; q += 2) {
               float a, c;
               pt_split(pt_fma2(pt_pair(v[32 * k + q], v[32 * k + q + 1]), sc2, z2), a, c);
-              a = pt_ex2(a);
-              c = pt_ex2(c);
+              a = ex2(a);
+              c = ex2(c);
               l2[(q >> 1) & 3] = pt_add2(l2[(q >> 1) & 3], pt_pair(a, c));
               const __nv_bfloat162 h = __floats2bfloat162_rn(a, c);
               pk[q >> 1] = *reinterpret_cast<const uint32_t *>(&h);
@@ -951,8 +946,7 @@ static bool bf16_map(CUtensorMap *m, const void *base, int nd, const int64_t *di
 template <int D, int MOD>
 static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
   static_assert(pt_smem<D>() <= 227 * 1024, "fits an SM");
-  ECHO_CUDA_OK(cudaFuncSetAttribute(paged_prefill_tc_kernel<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)pt_smem<D>()));
+  ECHO_CUDA_OK((allow_smem<paged_prefill_tc_kernel<D, MOD>>(pt_smem<D>())));
   int box = std::min(P.C.page_tokens & -P.C.page_tokens, PT_KEYS), qbox = 128 % P.G == 0 ? 128 / P.G : 0;
   CUtensorMap kmap = {}, vmap = {}, qmap = {};
   {
@@ -972,16 +966,7 @@ static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
   const int grid = std::min(sm_count(), PF_MAX_CTAS);
   paged_prefill_tc_kernel<D, MOD><<<grid, PT_THREADS, pt_smem<D>(), st>>>(P, kmap, vmap, qmap, box, qbox);
   ECHO_LAUNCH_OK();
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, std::max(1, std::min(16, P.prows / 16)));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // starts up while the first kernel ends
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  ECHO_CUDA_OK(cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D>, P));
+  ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<D>, dim3(grid, std::max(1, std::min(16, P.prows / 16))), dim3(128), st, P));
   return ECHO_OK;
 }
 

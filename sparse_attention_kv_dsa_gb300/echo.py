@@ -453,27 +453,31 @@ def _i32(t, shape, dev, where: str, name: str):
 def _paged(k_pages, v_pages, page_table, seq_len, status, where: str):
     """echo_paged_kv_t of k_pages and v_pages [n_pages, page_tokens, Hkv, d]: any strides with
     a unit last one, the same for both (pages laid out heads first are a transposed view)."""
-    dev = k_pages.device
+    dev, shape, dt = k_pages.device, k_pages.shape, k_pages.dtype
     if dev.type != "cuda" or dev.index != torch.cuda.current_device():
         _bad(where, "k_pages: on the current CUDA device")
-    shape = k_pages.shape
-    if (len(shape) != 4 or v_pages.shape != shape or k_pages.dtype is not v_pages.dtype or v_pages.device != dev
-            or 0 in shape):
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dt or v_pages.device != dev:
         _bad(where, "k_pages, v_pages: [n_pages, page_tokens, Hkv, d] of one shape, type and device")
-    if k_pages.dtype is torch.bfloat16:
-        dt = BF16
-    elif k_pages.dtype is torch.float32:
-        dt = F32
-    else:
-        raise EchoError(ERR_UNSUPPORTED, f"{where} (bfloat16 or float32)")
-    ks = [s if n > 1 else 0 for s, n in zip(k_pages.stride(), shape)]
-    if ks != [s if n > 1 else 0 for s, n in zip(v_pages.stride(), shape)] or (ks[3] != 1 and shape[3] > 1):
+    n_pages, T, Hkv, d = shape
+    ks, vs = k_pages.stride(), v_pages.stride()
+    if n_pages < 2 or T < 2 or Hkv < 2 or d < 2:           # a dimension of one entry has any stride
+        ks, vs = ([s if n > 1 else 0 for s, n in zip(x, shape)] for x in (ks, vs))
+    if ks != vs or (ks[3] != 1 and d > 1):
         _bad(where, "k_pages, v_pages: the same strides, the last one 1")
-    if page_table.dim() != 2 or 0 in page_table.shape or seq_len.dim() != 1 or seq_len.shape[0] != page_table.shape[0]:
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise EchoError(ERR_UNSUPPORTED, f"{where} (bfloat16 or float32)")
+    if page_table.dim() != 2 or seq_len.dim() != 1 or seq_len.shape[0] != page_table.shape[0]:
         _bad(where, "page_table: [B, max_pages], seq_len: [B]")
-    return PagedKVT(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], shape[0], shape[1], shape[2],
-                    shape[3], dt, page_table.shape[1], _i32(page_table, page_table.shape, dev, where, "page_table"),
+    return PagedKVT(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], n_pages, T, Hkv, d,
+                    BF16 if dt is torch.bfloat16 else F32, page_table.shape[1],
+                    _i32(page_table, page_table.shape, dev, where, "page_table"),
                     _i32(status, (1,), dev, where, "status"))
+
+
+def _stream(stream, dev) -> int:
+    """Handle of the stream, or of the device's current one (without the object that
+    torch.cuda.current_stream makes: 3 us)."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _head_rows(t, N: int, d: int, pages, where: str, name: str) -> int:
@@ -498,7 +502,7 @@ def _attn_buffers(q, out, lse, workspace, nbytes: int, stream, where: str):
     """out, lse and the workspace: the caller's, or new ones."""
     new = []
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         new.append(out)
     elif out.shape != q.shape or out.dtype is not q.dtype or out.device != q.device or not out.is_contiguous():
         _bad(where, f"out: contiguous, {list(q.shape)}, as q")
@@ -550,7 +554,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_len, *, q=None, q_out=N
         max_pos, rot = cos_sin.shape
     check(lib().echo_paged_append(ctypes.byref(c), ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, ptr(q_out),
                                   _i32(q_start, (B + 1,), dev, w, "q_start"), _i32(seq_len, (B,), dev, w, "seq_len"),
-                                  N, B, Hq, ptr(cos_sin), max_pos, rot, interleaved, stream_handle(stream)), w)
+                                  N, B, Hq, ptr(cos_sin), max_pos, rot, interleaved, _stream(stream, dev)), w)
     return q_out
 
 
@@ -571,7 +575,7 @@ def paged_attn_decode(q, k_pages, v_pages, page_table, seq_len, scale: float, *,
     out, lse, workspace = _attn_buffers(q, out, lse, workspace, nbytes, stream, w)
     check(L.echo_paged_attn_decode(ctypes.byref(c), q.data_ptr(), qs, _i32(seq_len, (B,), dev, w, "seq_len"), B, Hq,
                                    ctypes.byref(sc), out.data_ptr(), lse.data_ptr(), ptr(workspace),
-                                   workspace.nbytes if workspace is not None else 0, stream_handle(stream)), w)
+                                   workspace.nbytes if workspace is not None else 0, _stream(stream, dev)), w)
     return out, lse
 
 
@@ -596,5 +600,5 @@ def paged_attn_prefill(q, q_start, k_pages, v_pages, page_table, seq_len, scale:
     check(L.echo_paged_attn_prefill(ctypes.byref(c), q.data_ptr(), qs, _i32(q_start, (B + 1,), dev, w, "q_start"),
                                     _i32(seq_len, (B,), dev, w, "seq_len"), N, B, Hq, ctypes.byref(sc),
                                     out.data_ptr(), lse.data_ptr(), ptr(workspace),
-                                    workspace.nbytes if workspace is not None else 0, stream_handle(stream)), w)
+                                    workspace.nbytes if workspace is not None else 0, _stream(stream, dev)), w)
     return out, lse
