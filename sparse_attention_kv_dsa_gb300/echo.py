@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -439,89 +440,101 @@ def expand_block_slots(sel_blk, block_slot, seq_len, T: int, out, stream=None):
 
 
 # ------------------------------------------------------------- paged KV cache --
+# A small call of these is bound by host time, so the checks ask each tensor once for what they
+# need, and the structs are packed (PagedKVT and AttnScoresT in half the time).
+_PAGED = struct.Struct("@PPqqqiiiiiiPP")
+_SCORES = struct.Struct("@ffPiPP")
+_BF, _FL, _INT = torch.bfloat16, torch.float32, torch.int32
+
+
 def _bad(where: str, what: str):
     raise EchoError(ERR_INVALID_ARG, f"{where} ({what})")
 
 
-def _i32(t, shape, dev, where: str, name: str):
-    """A contiguous int32 tensor of this shape on this device, or None."""
-    if t is not None and (t.dtype is not torch.int32 or t.shape != shape or t.device != dev or not t.is_contiguous()):
-        _bad(where, f"{name}: contiguous int32 {list(shape)} on {dev}")
-    return ptr(t)
+def _vec(t, n: int, dt, dev: int, where: str, name: str) -> int:
+    """Address of a contiguous vector of n entries on this device; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dt or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        _bad(where, f"{name}: contiguous {dt} [{n}] on the cache's device")
+    return t.data_ptr()
 
 
-def _paged(k_pages, v_pages, page_table, seq_len, status, where: str):
-    """echo_paged_kv_t of k_pages and v_pages [n_pages, page_tokens, Hkv, d]: any strides with
-    a unit last one, the same for both (pages laid out heads first are a transposed view)."""
-    dev, shape, dt = k_pages.device, k_pages.shape, k_pages.dtype
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+def _paged(k_pages, v_pages, page_table, status, where: str):
+    """(echo_paged_kv_t, device, KV heads, d, type, B) of k_pages and v_pages
+    [n_pages, page_tokens, Hkv, d]: any strides with a unit last one, the same for both (pages
+    laid out heads first are a transposed view)."""
+    dev, dt, shape = k_pages.get_device(), k_pages.dtype, k_pages.shape
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         _bad(where, "k_pages: on the current CUDA device")
-    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dt or v_pages.device != dev:
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dt or v_pages.get_device() != dev:
         _bad(where, "k_pages, v_pages: [n_pages, page_tokens, Hkv, d] of one shape, type and device")
     n_pages, T, Hkv, d = shape
     ks, vs = k_pages.stride(), v_pages.stride()
     if n_pages < 2 or T < 2 or Hkv < 2 or d < 2:           # a dimension of one entry has any stride
-        ks, vs = ([s if n > 1 else 0 for s, n in zip(x, shape)] for x in (ks, vs))
+        ks, vs = (tuple(s if n > 1 else 0 for s, n in zip(x, shape)) for x in (ks, vs))
     if ks != vs or (ks[3] != 1 and d > 1):
         _bad(where, "k_pages, v_pages: the same strides, the last one 1")
-    if dt is not torch.bfloat16 and dt is not torch.float32:
+    if dt is not _BF and dt is not _FL:
         raise EchoError(ERR_UNSUPPORTED, f"{where} (bfloat16 or float32)")
-    if page_table.dim() != 2 or seq_len.dim() != 1 or seq_len.shape[0] != page_table.shape[0]:
-        _bad(where, "page_table: [B, max_pages], seq_len: [B]")
-    return PagedKVT(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], n_pages, T, Hkv, d,
-                    BF16 if dt is torch.bfloat16 else F32, page_table.shape[1],
-                    _i32(page_table, page_table.shape, dev, where, "page_table"),
-                    _i32(status, (1,), dev, where, "status"))
+    tab = page_table.shape
+    if len(tab) != 2 or page_table.dtype is not _INT or page_table.get_device() != dev or not page_table.is_contiguous():
+        _bad(where, "page_table: contiguous int32 [B, max_pages] on the cache's device")
+    c = _PAGED.pack(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], n_pages, T, Hkv, d,
+                    BF16 if dt is _BF else F32, tab[1], page_table.data_ptr(),
+                    0 if status is None else _vec(status, 1, _INT, dev, where, "status"))
+    return c, dev, Hkv, d, dt, tab[0]
 
 
-def _stream(stream, dev) -> int:
-    """Handle of the stream, or of the device's current one (without the object that
-    torch.cuda.current_stream makes: 3 us)."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
-
-
-def _head_rows(t, N: int, d: int, pages, where: str, name: str) -> int:
-    """Row stride of packed heads t [N, H, d]: a row's heads are contiguous, rows may be strided."""
-    if t.dim() != 3 or t.shape[0] != N or t.shape[2] != d or t.dtype is not pages.dtype or t.device != pages.device:
+def _head_rows(t, N: int, d: int, dt, dev: int, where: str, name: str):
+    """(heads, row stride) of packed heads t [N, H, d]: a row's heads are contiguous, rows may be
+    strided."""
+    n, H, e = t.shape if t.dim() == 3 else (-1, 0, 0)
+    if n != N or e != d or t.dtype is not dt or t.get_device() != dev:
         _bad(where, f"{name}: [{N}, H, {d}], the cache's type and device")
     s = t.stride()
-    if s[2] != 1 or (s[1] != d and t.shape[1] > 1):
+    if s[2] != 1 or (s[1] != d and H > 1):
         _bad(where, f"{name}: the heads of a row contiguous")
-    return s[0] if N > 1 else t.shape[1] * d
+    return H, s[0] if N > 1 else H * d
 
 
-def _attn_scores(scale, softcap, window, slopes, first_tok, prefix_len, rows: int, B: int, Hq: int, dev, where: str):
-    if slopes is not None and (slopes.dtype is not torch.float32 or slopes.shape != (Hq,) or slopes.device != dev
-                               or not slopes.is_contiguous()):
-        _bad(where, f"slopes: contiguous float32 [{Hq}] on {dev}")
-    return AttnScoresT(scale, softcap, ptr(slopes), window, _i32(first_tok, (rows,), dev, where, "first_tok"),
-                       _i32(prefix_len, (B,), dev, where, "prefix_len"))
+def _attn_scores(scale, softcap, window, slopes, first_tok, prefix_len, rows: int, B: int, Hq: int, dev: int, where: str):
+    if slopes is first_tok is prefix_len is None:
+        return _SCORES.pack(scale, softcap, 0, window, 0, 0)
+    return _SCORES.pack(scale, softcap, _vec(slopes, Hq, _FL, dev, where, "slopes"), window,
+                        _vec(first_tok, rows, _INT, dev, where, "first_tok"),
+                        _vec(prefix_len, B, _INT, dev, where, "prefix_len"))
+
+
+def _like(t, q, dt, shape, where: str, name: str):
+    if t.dtype is not dt or t.get_device() != q.get_device() or t.shape != shape or not t.is_contiguous():
+        _bad(where, f"{name}: contiguous {dt} {list(shape)} on q's device")
+    return t
 
 
 def _attn_buffers(q, out, lse, workspace, nbytes: int, stream, where: str):
     """out, lse and the workspace: the caller's, or new ones."""
-    new = []
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        new.append(out)
-    elif out.shape != q.shape or out.dtype is not q.dtype or out.device != q.device or not out.is_contiguous():
-        _bad(where, f"out: contiguous, {list(q.shape)}, as q")
-    if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        new.append(lse)
-    elif (lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or lse.device != q.device
-          or not lse.is_contiguous()):
-        _bad(where, f"lse: contiguous float32 {list(q.shape[:2])}")
+    shape, dev = q.shape, q.device
+    o = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else _like(out, q, q.dtype, shape, where, "out")
+    l = torch.empty(shape[:2], dtype=_FL, device=dev) if lse is None else _like(lse, q, _FL, shape[:2], where, "lse")
     if workspace is None:
-        if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-            new.append(workspace)
-    elif workspace.device != q.device or not workspace.is_contiguous():
-        _bad(where, "workspace: contiguous, on q's device")
+        w = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        w = workspace
+        if w.device != dev or not w.is_contiguous():
+            _bad(where, "workspace: contiguous, on q's device")
+        nbytes = w.nbytes
     if stream is not None:
-        for t in new:
-            t.record_stream(stream)
-    return out, lse, workspace
+        for t, given in ((o, out), (l, lse), (w, workspace)):
+            if given is None:
+                t.record_stream(stream)
+    return o, l, w, nbytes
+
+
+def _stream(stream, dev: int) -> int:
+    """Handle of the stream, or of the device's current one (without the object that
+    torch.cuda.current_stream makes: 3 us)."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
 def paged_append(k, v, k_pages, v_pages, page_table, seq_len, *, q=None, q_out=None, cos_sin=None,
@@ -531,30 +544,32 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_len, *, q=None, q_out=N
     goes to q_out (allocated if not given), which is returned.  seq_len [B] counts the new
     tokens; q_start [B + 1] gives each sequence's rows (None: one row each)."""
     w = "paged_append"
-    c = _paged(k_pages, v_pages, page_table, seq_len, status, w)
-    dev, B, N, d = k_pages.device, page_table.shape[0], k.shape[0], c.head_dim
-    ks, vs = _head_rows(k, N, d, k_pages, w, "k"), _head_rows(v, N, d, k_pages, w, "v")
-    if k.shape[1] != c.n_kv_heads or v.shape[1] != c.n_kv_heads:
-        _bad(w, f"k, v: [N, {c.n_kv_heads}, {d}]")
-    Hq = qs = 0
+    c, dev, Hkv, d, dt, B = _paged(k_pages, v_pages, page_table, status, w)
+    N = k.shape[0] if k.dim() else 0
+    kh, ks = _head_rows(k, N, d, dt, dev, w, "k")
+    vh, vs = _head_rows(v, N, d, dt, dev, w, "v")
+    if kh != Hkv or vh != Hkv:
+        _bad(w, f"k, v: [N, {Hkv}, {d}]")
+    Hq = qs = qp = op = 0
     if q is not None:
-        qs, Hq = _head_rows(q, N, d, k_pages, w, "q"), q.shape[1]
+        Hq, qs = _head_rows(q, N, d, dt, dev, w, "q")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
             if stream is not None:
                 q_out.record_stream(stream)
-        elif q_out.shape != q.shape or q_out.dtype is not q.dtype or q_out.device != dev or not q_out.is_contiguous():
-            _bad(w, "q_out: contiguous, as q")
+        else:
+            _like(q_out, q, dt, q.shape, w, "q_out")
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         _bad(w, "q_out without q")
-    rot = max_pos = 0
+    rot = max_pos = cp = 0
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype is not torch.float32 or cos_sin.device != dev or not cos_sin.is_contiguous():
-            _bad(w, "cos_sin: contiguous float32 [max_pos, rot_dim]")
-        max_pos, rot = cos_sin.shape
-    check(lib().echo_paged_append(ctypes.byref(c), ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, ptr(q_out),
-                                  _i32(q_start, (B + 1,), dev, w, "q_start"), _i32(seq_len, (B,), dev, w, "seq_len"),
-                                  N, B, Hq, ptr(cos_sin), max_pos, rot, interleaved, _stream(stream, dev)), w)
+        if cos_sin.dim() != 2 or cos_sin.dtype is not _FL or cos_sin.get_device() != dev or not cos_sin.is_contiguous():
+            _bad(w, "cos_sin: contiguous float32 [max_pos, rot_dim] on the cache's device")
+        (max_pos, rot), cp = cos_sin.shape, cos_sin.data_ptr()
+    check(lib().echo_paged_append(c, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, op,
+                                  _vec(q_start, B + 1, _INT, dev, w, "q_start"), _vec(seq_len, B, _INT, dev, w, "seq_len"),
+                                  N, B, Hq, cp, max_pos, rot, interleaved, _stream(stream, dev)), w)
     return q_out
 
 
@@ -566,16 +581,14 @@ def paged_attn_decode(q, k_pages, v_pages, page_table, seq_len, scale: float, *,
                       slopes=None, first_tok=None, prefix_len=None, out=None, lse=None, workspace=None, status=None,
                       stream=None):
     """Attention of one new token per sequence, q [B, Hq, d], over its pages -> (out, lse)."""
-    w = "paged_attn_decode"
-    c = _paged(k_pages, v_pages, page_table, seq_len, status, w)
-    B, Hq, dev, L = page_table.shape[0], q.shape[1], k_pages.device, lib()
-    qs = _head_rows(q, B, c.head_dim, k_pages, w, "q")
+    w, L = "paged_attn_decode", lib()
+    c, dev, Hkv, d, dt, B = _paged(k_pages, v_pages, page_table, status, w)
+    Hq, qs = _head_rows(q, B, d, dt, dev, w, "q")
     sc = _attn_scores(scale, softcap, window, slopes, first_tok, prefix_len, B, B, Hq, dev, w)
-    nbytes = L.echo_paged_decode_workspace_bytes(Hq, c.n_kv_heads, c.head_dim) if workspace is None else 0
-    out, lse, workspace = _attn_buffers(q, out, lse, workspace, nbytes, stream, w)
-    check(L.echo_paged_attn_decode(ctypes.byref(c), q.data_ptr(), qs, _i32(seq_len, (B,), dev, w, "seq_len"), B, Hq,
-                                   ctypes.byref(sc), out.data_ptr(), lse.data_ptr(), ptr(workspace),
-                                   workspace.nbytes if workspace is not None else 0, _stream(stream, dev)), w)
+    nbytes = L.echo_paged_decode_workspace_bytes(Hq, Hkv, d) if workspace is None else 0
+    out, lse, workspace, nbytes = _attn_buffers(q, out, lse, workspace, nbytes, stream, w)
+    check(L.echo_paged_attn_decode(c, q.data_ptr(), qs, _vec(seq_len, B, _INT, dev, w, "seq_len"), B, Hq, sc,
+                                   out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream, dev)), w)
     return out, lse
 
 
@@ -588,17 +601,16 @@ def paged_attn_prefill(q, q_start, k_pages, v_pages, page_table, seq_len, scale:
                        workspace=None, status=None, stream=None):
     """Attention of the packed new tokens q [N, Hq, d] (rows q_start[b] .. q_start[b+1]-1 are
     sequence b's last tokens) over their sequences' pages -> (out, lse)."""
-    w = "paged_attn_prefill"
-    c = _paged(k_pages, v_pages, page_table, seq_len, status, w)
-    N, B, Hq, dev, L = q.shape[0], page_table.shape[0], q.shape[1], k_pages.device, lib()
-    qs = _head_rows(q, N, c.head_dim, k_pages, w, "q")
+    w, L = "paged_attn_prefill", lib()
+    c, dev, Hkv, d, dt, B = _paged(k_pages, v_pages, page_table, status, w)
+    N = q.shape[0] if q.dim() else 0
+    Hq, qs = _head_rows(q, N, d, dt, dev, w, "q")
     if q_start is None:
         _bad(w, "q_start: int32 [B + 1]")
     sc = _attn_scores(scale, softcap, window, slopes, first_tok, prefix_len, N, B, Hq, dev, w)
-    nbytes = L.echo_paged_prefill_workspace_bytes(N, B, Hq, c.n_kv_heads, c.head_dim) if workspace is None else 0
-    out, lse, workspace = _attn_buffers(q, out, lse, workspace, nbytes, stream, w)
-    check(L.echo_paged_attn_prefill(ctypes.byref(c), q.data_ptr(), qs, _i32(q_start, (B + 1,), dev, w, "q_start"),
-                                    _i32(seq_len, (B,), dev, w, "seq_len"), N, B, Hq, ctypes.byref(sc),
-                                    out.data_ptr(), lse.data_ptr(), ptr(workspace),
-                                    workspace.nbytes if workspace is not None else 0, _stream(stream, dev)), w)
+    nbytes = L.echo_paged_prefill_workspace_bytes(N, B, Hq, Hkv, d) if workspace is None else 0
+    out, lse, workspace, nbytes = _attn_buffers(q, out, lse, workspace, nbytes, stream, w)
+    check(L.echo_paged_attn_prefill(c, q.data_ptr(), qs, _vec(q_start, B + 1, _INT, dev, w, "q_start"),
+                                    _vec(seq_len, B, _INT, dev, w, "seq_len"), N, B, Hq, sc, out.data_ptr(),
+                                    lse.data_ptr(), workspace.data_ptr(), nbytes, _stream(stream, dev)), w)
     return out, lse

@@ -80,6 +80,11 @@ def test_struct_layouts_and_workspaces():
     out = (ctypes.c_size_t * 2)()
     E.lib().echo_paged_struct_sizes(out)
     assert list(out) == [ctypes.sizeof(E.PagedKVT), ctypes.sizeof(E.AttnScoresT)]
+    assert list(out) == [E._PAGED.size, E._SCORES.size]
+    # the packed forms that the binding passes are the structs, field by field
+    assert E._PAGED.pack(*range(1, 14)) == bytes(E.PagedKVT(*range(1, 14)))
+    a, b = E._SCORES.pack(0.5, 2.0, 3, 4, 5, 6), bytes(E.AttnScoresT(0.5, 2.0, 3, 4, 5, 6))
+    assert [a[i:i + 4] for i in (0, 4, 8, 16, 24, 32)] == [b[i:i + 4] for i in (0, 4, 8, 16, 24, 32)]
     assert E.paged_decode_workspace_bytes(64, 8, 128) > 0
     assert E.paged_decode_workspace_bytes(7, 2, 128) == 0
     # one bound for every batch and length: it depends on the heads alone
