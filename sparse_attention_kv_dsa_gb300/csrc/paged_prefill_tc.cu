@@ -174,6 +174,11 @@ __device__ __forceinline__ uint64_t pt_fma2(uint64_t a, uint64_t b, uint64_t c) 
   asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t pt_mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t pt_add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -588,20 +593,19 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     if (warp == 10) cp_async_wait_all();
     if (warp == 8 && pt_elect()) {
     // ------------------------------------------------------------------ MMA --
+      // One thread issues everything, and the tensor cores wait whenever it is late: what can be
+      // waited for early (the keys of unit x + 1 and the values of x) is, before the weights of
+      // x; a tile's PV(x) and QK(x + 1) then go out together, and the commits after them.
       constexpr uint32_t id_qk = instr_desc(FMT_BF16, FMT_BF16, 0, 0, 128, 128);
       constexpr uint32_t id_pv = instr_desc(FMT_BF16, FMT_BF16, 0, 1, 128, D);
-      int nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
-      auto qk = [&](int t, int x, bool first, bool last) {
-        if (first) {
-          if (!pt_wait1(&S.qfull[t], nq[t] & 1)) { ok = false; return; }
-          ++nq[t];
-        }
-        const int g = 2 * x, sl = g % SLOTS;
-        if (!pt_wait1(&S.full[sl], (g / SLOTS) & 1)) { ok = false; return; }
-        fence_proxy_async_smem();                         // the loaders' cp.async writes, for the tensor cores
-        tc_fence_after();
-        const uint64_t ad = smem_desc(smem_u32(R + t * QB), 16, 1024, LAYOUT_SW128);
-        const uint64_t bd = smem_desc(smem_u32(R + (2 + sl) * QB), 16, 1024, LAYOUT_SW128);
+      const uint32_t ring = smem_u32(R + 2 * QB);
+      const uint64_t qd = smem_desc(smem_u32(R), 16, 1024, LAYOUT_SW128);
+      const uint64_t kd = smem_desc(ring, 16, 1024, LAYOUT_SW128);
+      const uint64_t vd = smem_desc(ring, 128 * 128, 1024, LAYOUT_SW128);
+      // slots and phases: keys of the unit whose scores come next, values of unit x
+      uint32_t ks = 0, kph = 0, vs = 1, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, no[2] = {0, 0};
+      auto qk = [&](int t, bool last) {
+        const uint64_t ad = qd + (uint64_t)(t * (QB >> 4)), bd = kd + (uint64_t)(ks * (QB >> 4));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t o = (uint32_t)((k >> 2) * 1024 + (k & 3) * 2);
@@ -610,23 +614,34 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         mma_commit(&S.sfull[t]);
         if (last) mma_commit(&S.qempty[t]);
       };
-      auto pv = [&](int t, int x, bool first) {
-        if (!pt_wait1(&S.pfull[t], np[t] & 1)) { ok = false; return; }
-        ++np[t];
+      auto pv = [&](int t, bool first) {
+        if (!pt_wait1(&S.pfull[t], pph[t])) { ok = false; return; }
+        pph[t] ^= 1;
         if (first) {
           if (no[t] && !pt_wait1(&S.oempty[t], (no[t] - 1) & 1)) { ok = false; return; }
           ++no[t];
         }
-        const int g = 2 * x + 1, sl = g % SLOTS;
-        if (!pt_wait1(&S.full[sl], (g / SLOTS) & 1)) { ok = false; return; }
-        fence_proxy_async_smem();
         tc_fence_after();
-        const uint32_t sa = smem_u32(R + (2 + sl) * QB);
+        const uint64_t bd = vd + (uint64_t)(vs * (QB >> 4));
 #pragma unroll
         for (int k = 0; k < PT_KEYS / 16; ++k)
-          pt_mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * k,
-                    smem_desc(sa + (uint32_t)(k * 2048), 128 * 128, 1024, LAYOUT_SW128), id_pv, (!first || k) ? 1u : 0u);
-        mma_commit(&S.pvdone[t]);
+          pt_mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * k, bd + 128 * k, id_pv, (!first || k) ? 1u : 0u);
+      };
+      auto wait_keys = [&]() {
+        ok = ok && pt_wait1(&S.full[ks], kph);
+        fence_proxy_async_smem();                         // the loaders' cp.async writes, for the tensor cores
+        tc_fence_after();
+      };
+      auto free_keys = [&]() {
+        mma_commit(&S.empty[ks]);
+        ks += 2;
+        if (ks >= SLOTS) { ks = 0; kph ^= 1; }
+      };
+      auto wait_queries = [&](int t) {
+        ok = ok && pt_wait1(&S.qfull[t], qph[t]);
+        qph[t] ^= 1;
+        fence_proxy_async_smem();
+        tc_fence_after();
       };
       int nitem = 0, left = 0;                            // units of the row tile from unit x on
       bool two = false;
@@ -640,28 +655,44 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         ++nitem;
         return i1 >= 0;
       };
-      if (take()) {
-        qk(0, 0, true, left == 1);
-        if (ok && two) qk(1, 0, true, left == 1);
-        if (ok) mma_commit(&S.empty[0]);
-        bool first = true;                                // unit x is its row tile's first
-        for (int x = 0; ok; ++x) {
-          const bool fresh = left == 1, two_x = two;      // fresh: unit x + 1 begins a row tile
-          pv(0, x, first);
-          if (ok && !fresh) qk(0, x + 1, false, left == 2);
-          if (ok && two_x) pv(1, x, first);
+      bool go = take(), first = true, fresh = true;       // first: unit x is its row tile's first
+      while (go) {
+        if (fresh) {                                      // the first scores of a row tile
+          wait_keys();
+          wait_queries(0);
           if (!ok) break;
-          mma_commit(&S.empty[(2 * x + 1) % SLOTS]);
-          if (fresh) {
-            if (!take()) break;
-            qk(0, x + 1, true, left == 1);
-          } else {
-            --left;
+          qk(0, left == 1);
+          if (two) {
+            wait_queries(1);
+            if (!ok) break;
+            qk(1, left == 1);
           }
-          if (ok && two) qk(1, x + 1, fresh, left == 1);
+          free_keys();
+          first = true;
+        }
+        fresh = left == 1;                                // unit x + 1 begins a row tile
+        if (!fresh) wait_keys();
+        if (!ok || !pt_wait1(&S.full[vs], vph)) { ok = false; break; }
+        fence_proxy_async_smem();
+        pv(0, first);
+        if (!ok) break;
+        if (!fresh) qk(0, left == 2);
+        mma_commit(&S.pvdone[0]);
+        if (two) {
+          pv(1, first);
           if (!ok) break;
-          mma_commit(&S.empty[(2 * x + 2) % SLOTS]);
-          first = fresh;
+          if (!fresh) qk(1, left == 2);
+          mma_commit(&S.pvdone[1]);
+        }
+        mma_commit(&S.empty[vs]);
+        vs += 2;
+        if (vs >= SLOTS) { vs = 1; vph ^= 1; }
+        if (!fresh) {
+          free_keys();
+          --left;
+          first = false;
+        } else {
+          go = take();
         }
       }
     }
@@ -706,7 +737,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       }
       float slope = 0.f;
       if (BIAS && P.slopes && there) slope = __ldg(P.slopes + hd) * kPgLog2e;
-      const float posf = (float)pos;
       // tiles that every row of the warp sees whole: by its window, and by its prefix
       const int wa = __reduce_max_sync(0xffffffffu, there ? (int)(((unsigned)lo + PT_KEYS - 1) / PT_KEYS) : 0);
       const int wb = __reduce_min_sync(0xffffffffu, there ? (pos + 1) / PT_KEYS : 0x7fffffff);
@@ -728,11 +758,47 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           uint32_t tag = pt_acquire(&S.vmtag[x % PT_VM]);
           const bool whole = ((ti >= wa && ti < wb) || (ti >= pa && ti < pb)) && tag == 2u * (uint32_t)(x + 1) + 1u;
           tmem_wait_ld();
-          if (CAP || BIAS) {
+          if (CAP) {
+            // u = s a, then tanh by its polynomial where every score of the warp is small enough
+            // (seven FMA-pipe operations, two scores each): the power and the reciprocal of the
+            // general form take 12 cycles of the special-function unit a score
+            const uint64_t a2 = pt_pair(P.f.a, P.f.a);
+            float um = 0.f;
 #pragma unroll
-            for (int k = 0; k < 128; ++k) {
-              v[k] = CAP ? score_log2(P.f, v[k]) : v[k] * P.f.a;
-              if (BIAS) v[k] = fmaf(-slope, fabsf(posf - (float)(t0 + k)), v[k]);
+            for (int k = 0; k < 128; k += 2) {
+              pt_split(pt_mul2(pt_pair(v[k], v[k + 1]), a2), v[k], v[k + 1]);
+              um = pt_max3(um, fabsf(v[k]), fabsf(v[k + 1]));
+            }
+            if (__all_sync(0xffffffffu, um * um <= kTanhW)) {
+              const uint64_t c5 = pt_pair(kTanh5, kTanh5), c4 = pt_pair(kTanh4, kTanh4), c3 = pt_pair(kTanh3, kTanh3),
+                             c2 = pt_pair(kTanh2, kTanh2), c1 = pt_pair(kTanh1, kTanh1);
+#pragma unroll
+              for (int k = 0; k < 128; k += 2) {
+                const uint64_t u = pt_pair(v[k], v[k + 1]), w = pt_mul2(u, u);
+                uint64_t p = pt_fma2(w, c5, c4);
+                p = pt_fma2(w, p, c3);
+                p = pt_fma2(w, p, c2);
+                p = pt_fma2(w, p, c1);
+                pt_split(pt_fma2(pt_mul2(u, w), p, u), v[k], v[k + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 128; ++k) v[k] = tanh_ex2(v[k]);
+            }
+          }
+          if (BIAS) {
+            const float mul = CAP ? P.f.c : P.f.a;
+            if (pre == 0 || ti < wb) {
+              // no token behind a row's position counts: |p - t| = (p - t0) - k
+              const float d0 = -slope * (float)(pos - t0);
+              const uint64_t m2 = pt_pair(mul, mul), s2 = pt_pair(slope, slope), d2 = pt_pair(d0, d0);
+#pragma unroll
+              for (int k = 0; k < 128; k += 2)
+                pt_split(pt_fma2(pt_pair(v[k], v[k + 1]), m2, pt_fma2(s2, pt_pair((float)k, (float)(k + 1)), d2)), v[k], v[k + 1]);
+            } else {
+              const float d0 = (float)(pos - t0);
+#pragma unroll
+              for (int k = 0; k < 128; ++k) v[k] = fmaf(-slope, fabsf(d0 - (float)k), v[k] * mul);
             }
           }
           if (!whole) {                                   // the same in every lane
@@ -755,7 +821,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           mx4[0] = pt_max3(mx4[0], v[124], v[125]);
           mx4[1] = pt_max3(mx4[1], v[126], v[127]);
           float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          const float sc = (CAP || BIAS) ? 1.f : aa;
+          const float sc = BIAS ? 1.f : CAP ? P.f.c : aa;
           mx *= sc;
           // move the maximum when it is passed by 2^8, or was none
           const float nm = mx > m + 8.f ? mx : m;
