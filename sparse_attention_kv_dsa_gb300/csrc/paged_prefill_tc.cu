@@ -20,7 +20,7 @@
 // maximum passes it by 2^8 (the weights stay below 256, exact in the float32 sums), so O is
 // rescaled in TMEM a few times in a long row and not with every tile.
 // TMEM columns: S_0 0-127, S_1 128-255 (P_i in the first 64 of S_i), O_0 256.., O_1 384...
-// Warps 0-3 and 4-7: softmax and epilogue of tile 0 and 1 (200 registers: a row's 128 scores
+// Warps 0-3 and 4-7: softmax and epilogue of tile 0 and 1 (192 registers: a row's 128 scores
 // stay in registers); warp 8: MMA issue; warp 9: the walk over the units and their page-table
 // look-ups; warp 10: the queries; warps 12, 13: the keys; 14, 15: the values.  A tile of the cache whose 128
 // tokens are all seen by some row comes by TMA, in boxes of the largest power of two of rows
@@ -36,7 +36,7 @@
 
 namespace echo {
 
-constexpr int PT_THREADS = 512;      // four warpgroups of 128 registers: 200 + 200 + 64 + 48 after the split
+constexpr int PT_THREADS = 512;      // four warpgroups of 128 registers: 192 + 192 + 88 + 40 after the split
 constexpr int PT_KEYS = 128;
 constexpr int PT_ITEMS = 4;          // ring of row tiles in flight
 constexpr int PT_UNITS = 4;          // ring of units looked up
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
 
   if (warp >= 8) {
     if (warp >= 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
       // -------------------------------------------------------- keys, values --
       const int which = (warp - 12) >> 1, half = warp & 1;
       const CUtensorMap *map = which ? &vmap : &kmap;
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       for (int g = max(which, issued + 1 - SLOTS); !ok && g < issued; g += 2)
         pt_wait(&S.full[g % SLOTS], (g / SLOTS) & 1);
     } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // ------------------------------------------------------------ walk, queries --
     if (warp == 9) {
       int xt = S.found, b = 0, nitem = 0, i = 0;          // i: tile of the unit looked up next
@@ -595,7 +595,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     // ------------------------------------------------------------------ MMA --
       // One thread issues everything, and the tensor cores wait whenever it is late: what can be
       // waited for early (the keys of unit x + 1 and the values of x) is, before the weights of
-      // x; a tile's PV(x) and QK(x + 1) then go out together, and the commits after them.
+      // x; a tile's PV(x) and QK(x + 1) then go out together.  A commit behind other commits
+      // stalls until the products before it are done, so there is one a QK, and what else it
+      // sets free -- K(x), V(x - 1), a row tile's queries -- the softmax warps hand back when
+      // they wake up on it.
       constexpr uint32_t id_qk = instr_desc(FMT_BF16, FMT_BF16, 0, 0, 128, 128);
       constexpr uint32_t id_pv = instr_desc(FMT_BF16, FMT_BF16, 0, 1, 128, D);
       const uint32_t ring = smem_u32(R + 2 * QB);
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       const uint64_t vd = smem_desc(ring, 128 * 128, 1024, LAYOUT_SW128);
       // slots and phases: keys of the unit whose scores come next, values of unit x
       uint32_t ks = 0, kph = 0, vs = 1, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, no[2] = {0, 0};
-      auto qk = [&](int t, bool last) {
+      auto qk = [&](int t) {
         const uint64_t ad = qd + (uint64_t)(t * (QB >> 4)), bd = kd + (uint64_t)(ks * (QB >> 4));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -612,7 +615,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           mma_f16(tmem + 128u * t, ad + o, bd + o, id_qk, k ? 1u : 0u);
         }
         mma_commit(&S.sfull[t]);
-        if (last) mma_commit(&S.qempty[t]);
       };
       auto pv = [&](int t, bool first) {
         if (!pt_wait1(&S.pfull[t], pph[t])) { ok = false; return; }
@@ -632,8 +634,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         fence_proxy_async_smem();                         // the loaders' cp.async writes, for the tensor cores
         tc_fence_after();
       };
-      auto free_keys = [&]() {
-        mma_commit(&S.empty[ks]);
+      auto next_keys = [&]() {
         ks += 2;
         if (ks >= SLOTS) { ks = 0; kph ^= 1; }
       };
@@ -661,13 +662,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           wait_keys();
           wait_queries(0);
           if (!ok) break;
-          qk(0, left == 1);
+          qk(0);
           if (two) {
             wait_queries(1);
             if (!ok) break;
-            qk(1, left == 1);
+            qk(1);
           }
-          free_keys();
+          next_keys();
           first = true;
         }
         fresh = left == 1;                                // unit x + 1 begins a row tile
@@ -676,19 +677,18 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         fence_proxy_async_smem();
         pv(0, first);
         if (!ok) break;
-        if (!fresh) qk(0, left == 2);
-        mma_commit(&S.pvdone[0]);
+        if (!fresh) qk(0);
+        if (fresh) mma_commit(&S.pvdone[0]);               // the epilogue's
         if (two) {
           pv(1, first);
           if (!ok) break;
-          if (!fresh) qk(1, left == 2);
-          mma_commit(&S.pvdone[1]);
+          if (!fresh) qk(1);
+          if (fresh) mma_commit(&S.pvdone[1]);
         }
-        mma_commit(&S.empty[vs]);
         vs += 2;
         if (vs >= SLOTS) { vs = 1; vph ^= 1; }
         if (!fresh) {
-          free_keys();
+          next_keys();
           --left;
           first = false;
         } else {
@@ -699,13 +699,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     }
   } else {
     // -------------------------------------------------------------- softmax --
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int t = warp >> 2;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = trow + 128u * t, to = trow + 256u + 128u * t;
     const int r = t * 128 + (warp & 3) * 32 + lane;       // row of the row tile
     const float aa = fmaxf(P.f.a, 1e-37f);                // a scale of 0 keeps masked scores at -inf
-    int x = 0, nitem = 0, ns = 0;                         // units, row tiles and this tile's units so far
+    int x = 0, nitem = 0, ns = 0, nd = 0;                 // units, row tiles, this tile's units and row tiles so far
     while (ok) {
       const int e = nitem % PT_ITEMS;
       if (!pt_wait(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; break; }
@@ -721,6 +721,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       }
       const int len = I.len, n = I.n, nr = I.nr, r0 = I.r0, s0 = I.s0, kvh = I.kvh, elsewhere = I.elsewhere, c0 = I.c0;
       const TileSpan span = I.span;
+      const int last_t = nr > 128 ? 1 : 0;                // the tile whose products are issued last
       int pre = I.pre;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.iempty[e]);
@@ -746,6 +747,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       for (int i = i0; i < i1; ++i, ++x, ++ns) {
         if (!pt_wait(&S.sfull[t], ns & 1)) { ok = false; break; }
         tc_fence_after();
+        if ((warp & 3) == 0 && lane == 0) {                // every product up to this QK is done
+          if (t == last_t) {
+            mbar_arrive(&S.empty[(2 * x) % SLOTS]);
+            if (x > 0) mbar_arrive(&S.empty[(2 * x - 1) % SLOTS]);
+          }
+          if (i + 1 == i1) mbar_arrive(&S.qempty[t]);
+        }
         if (some) {
           const int ti = span.tile(i), t0 = ti * PT_KEYS;
           float v[128];
@@ -823,7 +831,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float sc = BIAS ? 1.f : CAP ? P.f.c : aa;
           mx *= sc;
-          // move the maximum when it is passed by 2^8, or was none
+          // move the maximum when it is passed by 2^8, or was none (PV of the tile before was
+          // issued ahead of this tile's QK: it is done)
           const float nm = mx > m + 8.f ? mx : m;
           if (i == i0) {
             m = mx;
@@ -831,8 +840,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
             const float corr = nm != m ? ex2(m - nm) : 1.f;
             m = nm;
             l *= corr;
-            if (!pt_wait(&S.pvdone[t], (ns - 1) & 1)) { ok = false; break; }
-            tc_fence_after();
 #pragma unroll 1
             for (int k = 0; k < D; k += 16) {
               uint32_t o[16];
@@ -875,7 +882,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       }
       if (!ok) break;
       // ---- epilogue
-      if (!pt_wait(&S.pvdone[t], (ns - 1) & 1)) { ok = false; break; }
+      if (!pt_wait(&S.pvdone[t], nd & 1)) { ok = false; break; }
+      ++nd;
       tc_fence_after();
       const bool done = elsewhere == 0;
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
