@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       uint32_t ks = 0, kph = 0, vs = 1, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, no[2] = {0, 0};
       auto qk = [&](int t) {
         const uint64_t ad = qd + (uint64_t)(t * (QB >> 4)), bd = kd + (uint64_t)(ks * (QB >> 4));
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t o = (uint32_t)((k >> 2) * 1024 + (k & 3) * 2);
           mma_f16(tmem + 128u * t, ad + o, bd + o, id_qk, k ? 1u : 0u);
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         }
         tc_fence_after();
         const uint64_t bd = vd + (uint64_t)(vs * (QB >> 4));
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < PT_KEYS / 16; ++k)
           pt_mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * k, bd + 128 * k, id_pv, (!first || k) ? 1u : 0u);
       };
