@@ -35,9 +35,269 @@ __device__ __forceinline__ SeqRows seq_rows(const PrefillParams &P, int b) {
   return r;
 }
 
-constexpr int PF_MAX_CTAS = 160;     // partial slots: two a CTA
-constexpr int PF_ROWS = 256;         // packed rows of a row tile of the tensor-core kernel
-constexpr int PF_MAX_B = 4096;       // sequences of a call
+constexpr int PF_MAX_CTAS = 320;     // partial slots: two a CTA
+constexpr int PF_MAX_ROWS = 256;     // packed rows of a row tile: 256 in bf16, 64 in float32
+constexpr int PF_MAX_B = 2048;       // sequences of a call
+constexpr int PF_ITEM_WEIGHT = 1;    // of a row tile besides its tiles of the cache, in units
+
+// A row tile of one KV head, and its part in a CTA's run of units.
+struct RowTile {
+  int b, kvh, s0, n, len, pre, r0, nr;
+  int first, lo, hi;                 // over its rows: smallest first token and lower end, past the last position
+  TileSpan span;
+  int i0, i1;                        // tiles of the span in this run; i1 < 0: the run is over
+  int elsewhere;                     // 1: begun in another CTA, 2: goes on in another
+  int c0;                            // CTA of its first unit
+};
+
+// What the rows of row tile rt of sequence b see.  Lanes of a warp share the rows when
+// `lanes` is 32 (all of them call); one thread walks them alone when it is 1.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ void row_tile_range(const PrefillParams &P, int b, int rt, RowTile &I, int lanes) {
+  const SeqRows R = seq_rows(P, b);
+  const int G = P.G;
+  I.b = b;
+  I.s0 = R.s0;
+  I.n = R.n;
+  I.len = paged_len(P.C, P.seq_len, b);
+  I.pre = P.prefix_len ? min(P.prefix_len[b], I.len) : 0;
+  I.r0 = rt * ROWS;
+  I.nr = (int)min((int64_t)ROWS, (int64_t)R.n * G - I.r0);
+  // tokens of the tile at positions >= 0
+  const int i0 = max(div_by(P.group, I.r0), I.n - I.len), i1 = div_by(P.group, I.r0 + I.nr - 1);
+  const int p0 = I.len - I.n;
+  int first = 0, lo = 0;
+  if (i1 < i0) {                                          // no row of the tile is there
+    first = lo = 0x7fffffff;
+    I.pre = 0;
+  } else if (P.first_tok) {
+    first = lo = 0x7fffffff;
+    for (int i = i0 + (lanes > 1 ? (int)(threadIdx.x & 31) : 0); i <= i1; i += lanes) {
+      const int f = max(__ldg(P.first_tok + R.s0 + i), 0);
+      first = min(first, f);
+      lo = min(lo, P.window ? max(f, p0 + i - P.window + 1) : f);
+    }
+    if (lanes > 1) {
+      first = __reduce_min_sync(0xffffffffu, first);
+      lo = __reduce_min_sync(0xffffffffu, lo);
+    }
+  } else if (P.window) {
+    lo = max(0, p0 + i0 - P.window + 1);
+  }
+  I.first = first;
+  I.lo = lo;
+  I.hi = i1 < i0 ? 0 : p0 + i1 + 1;
+  I.span = tile_span(first, I.pre, lo, I.hi, KEYS);
+  if (I.span.nA + I.span.nB == 0) I.span.nA = 1;          // nothing seen: one tile of zeros writes the empty rows
+}
+
+// Deals the units out: unit = one KEYS-token tile of the cache for one row tile of ROWS packed
+// rows of one KV head, ordered by (sequence, row tile, KV head, tile); a row tile begins with
+// PF_ITEM_WEIGHT units' worth of weight (its queries, its epilogue).  CTA c gets the weights
+// [per c, per (c + 1)): a tile belongs to the CTA that holds its last one.
+struct PlanShared {
+  long long sum[32];
+  long long before;                  // weight before row tile `found`
+  int found;                         // row tile in which the run begins, -1: no run
+  int tiles[PF_MAX_B + 1];           // row tiles before each sequence
+};
+struct RunPlan {
+  long long per, u0, u1;
+  int ntiles;
+};
+// Last sequence whose row tiles begin at or before x.
+__device__ __forceinline__ int plan_seq(const PlanShared &S, int B, int x) {
+  int a = 0, c = B - 1;
+  while (a < c) {
+    const int m = (a + c + 1) >> 1;
+    if (S.tiles[m] <= x) a = m; else c = m - 1;
+  }
+  return a;
+}
+// Inclusive sum over the block of v, and the block's total; the whole block calls it.
+template <int THREADS>
+__device__ __forceinline__ long long plan_scan(PlanShared &S, long long v, long long &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();
+  if (lane == 31) S.sum[warp] = v;
+  __syncthreads();
+  total = 0;
+#pragma unroll 4
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) v += S.sum[w];
+    total += S.sum[w];
+  }
+  return v;
+}
+template <int ROWS, int KEYS, int THREADS>
+__device__ __forceinline__ RunPlan prefill_plan(const PrefillParams &P, PlanShared &S) {
+  const int tid = threadIdx.x;
+  RunPlan pl;
+  if (tid == 0) S.found = -1;
+  long long base = 0, sum;
+  for (int b0 = 0; b0 < P.B; b0 += THREADS) {
+    const int b = b0 + tid;
+    const long long n = b < P.B ? ((int64_t)seq_rows(P, b).n * P.G + ROWS - 1) / ROWS : 0;
+    const long long end = base + plan_scan<THREADS>(S, n, sum);
+    if (b < P.B) S.tiles[b] = (int)(end - n);
+    base += sum;
+  }
+  if (tid == 0) S.tiles[P.B] = (int)base;
+  pl.ntiles = (int)base;
+  __syncthreads();
+  // two passes over the row tiles: the total, then the one that holds the CTA's first weight
+  long long total = 0, n = 0;
+  pl.per = pl.u0 = pl.u1 = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long at = 0;
+    for (int x0 = 0; x0 < pl.ntiles; x0 += THREADS) {
+      const int x = x0 + tid;
+      if (pass == 0 || pl.ntiles > THREADS) {             // few row tiles: the first pass's values still hold
+        n = 0;
+        if (x < pl.ntiles) {
+          RowTile I;
+          const int b = plan_seq(S, P.B, x);
+          row_tile_range<ROWS, KEYS>(P, b, x - S.tiles[b], I, 1);
+          n = (long long)(I.span.nA + I.span.nB + PF_ITEM_WEIGHT) * P.C.n_kv_heads;
+        }
+      }
+      const long long end = at + plan_scan<THREADS>(S, n, sum);
+      at += sum;
+      if (pass == 1 && end - n <= pl.u0 && pl.u0 < end) {
+        S.found = x;
+        S.before = end - n;
+      }
+      if (pass == 1 && pl.u0 < at) break;                 // the same in every thread
+    }
+    if (pass == 0) {
+      total = at;
+      pl.per = max((total + gridDim.x - 1) / (long long)gridDim.x, 1ll);
+      pl.u0 = pl.per * blockIdx.x;
+      pl.u1 = min(total, pl.u0 + pl.per);
+      if (pl.u0 >= total) break;
+    }
+  }
+  __syncthreads();
+  return pl;
+}
+
+// The walk over the row tiles of a CTA's run.  A whole warp moves it together.
+template <int ROWS, int KEYS>
+struct RowTileWalk {
+  const PrefillParams &P;
+  const PlanShared &S;
+  const RunPlan pl;
+  RowTile I;
+  int xt, b;
+  long long ws;                      // weight before the row tile
+
+  __device__ __forceinline__ void enter() {
+    while (b + 1 < P.B && S.tiles[b + 1] <= xt) ++b;
+    row_tile_range<ROWS, KEYS>(P, b, xt - S.tiles[b], I, 32);
+    if ((threadIdx.x & 31) == 0 && I.len < I.n) paged_fail(P.C.status, ECHO_ERR_INVALID_ARG);
+  }
+  __device__ __forceinline__ void part(int i0) {          // its tiles in this run; none: the run is over
+    const int nt = I.span.nA + I.span.nB;
+    I.i0 = i0;
+    I.i1 = (int)min((long long)nt, pl.u1 - ws - PF_ITEM_WEIGHT);
+    I.elsewhere = (I.i0 > 0 ? 1 : 0) | (I.i1 < nt ? 2 : 0);
+    I.c0 = (int)((ws + PF_ITEM_WEIGHT) / pl.per);
+    if (I.i1 <= I.i0) I.i1 = -1;
+  }
+  __device__ __forceinline__ RowTileWalk(const PrefillParams &p, const PlanShared &s, const RunPlan &r)
+      : P(p), S(s), pl(r), I(), xt(s.found), b(0), ws(0) {
+    I.i1 = -1;
+    if (xt < 0) return;
+    b = plan_seq(S, P.B, xt);
+    enter();
+    const int nt = I.span.nA + I.span.nB + PF_ITEM_WEIGHT;
+    I.kvh = (int)((pl.u0 - S.before) / nt);
+    ws = S.before + (long long)I.kvh * nt;
+    part(max(0, (int)(pl.u0 - ws) - PF_ITEM_WEIGHT));
+  }
+  __device__ __forceinline__ void next() {
+    ws += I.span.nA + I.span.nB + PF_ITEM_WEIGHT;
+    if (I.kvh + 1 < P.C.n_kv_heads) {
+      ++I.kvh;
+    } else if (++xt < pl.ntiles) {
+      I.kvh = 0;
+      enter();
+    } else {
+      I.i1 = -1;
+      return;
+    }
+    part(0);
+  }
+};
+
+// Leaves word that a split row tile ends in this CTA.
+__device__ __forceinline__ void join_record(const PrefillParams &P, int c0, int s0, int r0, int nr, int kvh) {
+  int32_t *rec = P.rec + blockIdx.x * 8;
+  rec[1] = c0;
+  rec[2] = s0;
+  rec[3] = r0;
+  rec[4] = nr;
+  rec[5] = kvh;
+  rec[0] = 1;
+}
+
+// Joins the partials of the row tile that ends in CTA blockIdx.x, in the order of their units:
+// slot 1 of its first CTA, then slot 0 of the following ones.  A warp takes a row: the maximum
+// of all first, so that the weighted sums are independent loads.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) paged_prefill_join_kernel(const __grid_constant__ PrefillParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c1 = blockIdx.x;
+  const int4 ra = *reinterpret_cast<const int4 *>(P.rec + c1 * 8), rb = *reinterpret_cast<const int4 *>(P.rec + c1 * 8 + 4);
+  if (ra.x == 0) return;
+  const int c0 = ra.y, s0 = ra.z, r0 = ra.w, nr = rb.x, kvh = rb.y, np = c1 - c0 + 1;
+  const int lane = threadIdx.x & 31;
+  constexpr int VL = D / 32;
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < nr; r += gridDim.y * 4) {
+    auto row = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * P.prows + r; };
+    float M = -INFINITY, L = 0.f, v[VL];
+    for (int i = lane; i < np; i += 32) M = fmaxf(M, P.pml[row(i) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+    for (int i = 0; i < VL; ++i) v[i] = 0.f;
+    const float z = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+      const float2 ml = *reinterpret_cast<const float2 *>(P.pml + row(i) * 2);
+      const float *o = P.po + row(i) * D + lane * VL;
+      float x[VL];
+      if constexpr (VL == 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(o);
+        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2 *>(o);
+        x[0] = f.x; x[1] = f.y;
+      }
+      const float w = ex2(ml.x - z);
+      L += w * ml.y;
+#pragma unroll
+      for (int e = 0; e < VL; ++e) v[e] = fmaf(w, x[e], v[e]);
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    const int tk = div_by(P.group, r0 + r), hd = kvh * P.G + (r0 + r) - tk * P.G;
+    const int64_t orow = (int64_t)(s0 + tk) * P.Hq + hd;
+    T *dst = (T *)P.out + orow * D + lane * VL;
+#pragma unroll
+    for (int i = 0; i < VL; i += 2) {
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<__nv_bfloat162 *>(dst + i) = __floats2bfloat162_rn(v[i] * inv, v[i + 1] * inv);
+      else
+        *reinterpret_cast<float2 *>(dst + i) = make_float2(v[i] * inv, v[i + 1] * inv);
+    }
+    if (lane == 0) P.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPgLn2;
+  }
+}
 
 echo_status_t launch_prefill_tc(PrefillParams &P, cudaStream_t st);
 

@@ -6,7 +6,7 @@
 // A persistent CTA per SM.  The work is dealt out in units -- one 128-token tile of the cache
 // for one row tile of 256 packed rows (token r / G, head r % G of the KV head's group) --
 // ordered by (sequence, row tile, KV head, tile); every CTA takes a run of them of equal
-// weight (a row tile begins with PT_ITEM_WEIGHT units' worth: its queries, its epilogue),
+// weight (a row tile begins with PF_ITEM_WEIGHT units' worth: its queries, its epilogue),
 // found from the device's own lengths and masks, so that ragged prompts, the triangle of a causal
 // mask and a few rows over a long cache all spread evenly.  A row tile whose units lie in
 // several CTAs leaves partials (two slots a CTA) that a second kernel joins in order.
@@ -37,21 +37,10 @@
 namespace echo {
 
 constexpr int PT_THREADS = 512;      // four warpgroups of 128 registers: 192 + 192 + 88 + 40 after the split
-constexpr int PT_KEYS = 128;
+constexpr int PT_ROWS = 256, PT_KEYS = 128;
 constexpr int PT_ITEMS = 4;          // ring of row tiles in flight
 constexpr int PT_UNITS = 4;          // ring of units looked up
 constexpr int PT_VM = 8;             // ring of the tiles' token masks
-constexpr int PT_ITEM_WEIGHT = 1;    // of a row tile besides its tiles, in units
-
-// A row tile's part in this CTA's run.
-struct PtItem {
-  int b, kvh, s0, n, len, pre, r0, nr;
-  int first, lo, hi;                 // over its rows: smallest first token and lower end, past the last position
-  TileSpan span;
-  int i0, i1;                        // tiles of the span in this run; i1 < 0: the run is over
-  int elsewhere;                     // 1: begun in another CTA, 2: goes on in another
-  int c0;                            // CTA of its first unit
-};
 
 template <int D>
 struct PtShape {
@@ -68,14 +57,11 @@ struct PtShared {
   int fail;
   uint32_t vm[PT_VM][4];             // tokens there, of unit x in entry x % PT_VM
   uint32_t vmtag[PT_VM];             // 2 (x + 1) + (all of them there)
-  PtItem item[PT_ITEMS];
+  RowTile item[PT_ITEMS];
   int64_t row[PT_UNITS][PT_KEYS];           // of a unit's tokens: offset of the row (-1: not there), and page
   int32_t page[PT_UNITS][PT_KEYS];
   int kvh[PT_UNITS], t0[PT_UNITS], whole[PT_UNITS];       // of a unit: KV head (-1: no more units), first token, every token there
-  long long warp[PT_THREADS / 32];
-  long long before;
-  int found;
-  int tiles[PF_MAX_B + 1];           // row tiles before each sequence
+  PlanShared plan;
 };
 
 template <int D>
@@ -205,45 +191,6 @@ __device__ __forceinline__ uint32_t pt_bits(int a, int b) {
   return hi & ~lo;
 }
 
-// What the rows of row tile rt of sequence b see.  Lanes of a warp share the rows when
-// `lanes` is 32 (all of them call); one thread walks them alone when it is 1.
-__device__ __forceinline__ void pt_range(const PrefillParams &P, int b, int rt, PtItem &I, int lanes) {
-  const SeqRows R = seq_rows(P, b);
-  const int G = P.G;
-  I.b = b;
-  I.s0 = R.s0;
-  I.n = R.n;
-  I.len = paged_len(P.C, P.seq_len, b);
-  I.pre = P.prefix_len ? min(P.prefix_len[b], I.len) : 0;
-  I.r0 = rt * PF_ROWS;
-  I.nr = (int)min((int64_t)PF_ROWS, (int64_t)R.n * G - I.r0);
-  const int i0 = max(I.r0 / G, I.n - I.len), i1 = (I.r0 + I.nr - 1) / G;   // tokens of the tile at positions >= 0
-  const int p0 = I.len - I.n;
-  int first = 0, lo = 0;
-  if (i1 < i0) {                                          // no row of the tile is there
-    first = lo = 0x7fffffff;
-    I.pre = 0;
-  } else if (P.first_tok) {
-    first = lo = 0x7fffffff;
-    for (int i = i0 + (lanes > 1 ? (int)(threadIdx.x & 31) : 0); i <= i1; i += lanes) {
-      const int f = max(__ldg(P.first_tok + R.s0 + i), 0);
-      first = min(first, f);
-      lo = min(lo, P.window ? max(f, p0 + i - P.window + 1) : f);
-    }
-    if (lanes > 1) {
-      first = __reduce_min_sync(0xffffffffu, first);
-      lo = __reduce_min_sync(0xffffffffu, lo);
-    }
-  } else if (P.window) {
-    lo = max(0, p0 + i0 - P.window + 1);
-  }
-  I.first = first;
-  I.lo = lo;
-  I.hi = i1 < i0 ? 0 : p0 + i1 + 1;
-  I.span = tile_span(first, I.pre, lo, I.hi, PT_KEYS);
-  if (I.span.nA + I.span.nB == 0) I.span.nA = 1;          // nothing seen: one tile of zeros writes the empty rows
-}
-
 template <int D, int MOD>
 __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const __grid_constant__ PrefillParams P,
                                                                         const __grid_constant__ CUtensorMap kmap,
@@ -258,7 +205,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
   PtShared &S = *reinterpret_cast<PtShared *>(R + (2 + SLOTS) * QB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const echo_paged_kv_t &C = P.C;
-  const int Hkv = C.n_kv_heads, G = P.G;
+  const int G = P.G;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -274,7 +221,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     for (int i = 0; i < PT_UNITS; ++i) { mbar_init(&S.ufull[i], 1); mbar_init(&S.uempty[i], 4); }
     for (int i = 0; i < PT_VM; ++i) S.vmtag[i] = 0;
     S.fail = 0;
-    S.found = -1;
     fence_mbar_init();
   }
   if (warp == 8) {
@@ -282,90 +228,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     tmem_relinquish();
   }
 
-  // ---- row tiles before each sequence
-  {
-    int base = 0;
-    for (int b0 = 0; b0 < P.B; b0 += PT_THREADS) {
-      const int b = b0 + tid;
-      const int n = b < P.B ? (int)(((int64_t)seq_rows(P, b).n * G + PF_ROWS - 1) / PF_ROWS) : 0;
-      int v = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-      }
-      __syncthreads();
-      if (lane == 31) S.warp[warp] = v;
-      __syncthreads();
-      int end = base + v;
-      for (int w = 0; w < PT_THREADS / 32; ++w) {
-        if (w < warp) end += (int)S.warp[w];
-        base += (int)S.warp[w];
-      }
-      if (b < P.B) S.tiles[b] = end - n;
-    }
-    __syncthreads();
-    if (tid == 0) S.tiles[P.B] = base;
-  }
-  __syncthreads();
-  const int ntiles = S.tiles[P.B];
-  auto seq_of = [&](int x) {                              // last sequence whose tiles begin at or before x
-    int a = 0, c = P.B - 1;
-    while (a < c) {
-      const int m = (a + c + 1) >> 1;
-      if (S.tiles[m] <= x) a = m; else c = m - 1;
-    }
-    return a;
-  };
-  auto units_of = [&](int x) -> long long {               // weight of row tile x, over the KV heads
-    PtItem I;
-    const int b = seq_of(x);
-    pt_range(P, b, x - S.tiles[b], I, 1);
-    return (long long)(I.span.nA + I.span.nB + PT_ITEM_WEIGHT) * Hkv;
-  };
-  long long mine = 0, keep = 0;
-  for (int x = tid; x < ntiles; x += PT_THREADS) {
-    keep = units_of(x);
-    mine += keep;
-  }
-  long long total = 0;
-  {
-    long long v = mine;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) S.warp[warp] = v;
-    __syncthreads();
-    for (int w = 0; w < PT_THREADS / 32; ++w) total += S.warp[w];
-  }
-  const long long per = max((total + gridDim.x - 1) / (long long)gridDim.x, 1ll);
-  const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
-  if (u0 < u1) {
-    long long base = 0;
-    for (int x0 = 0; x0 < ntiles; x0 += PT_THREADS) {
-      const int x = x0 + tid;
-      const long long n = x < ntiles ? (ntiles <= PT_THREADS ? keep : units_of(x)) : 0;
-      long long v = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-      }
-      __syncthreads();
-      if (lane == 31) S.warp[warp] = v;
-      __syncthreads();
-      long long end = base + v;
-      for (int w = 0; w < PT_THREADS / 32; ++w) {
-        if (w < warp) end += S.warp[w];
-        base += S.warp[w];
-      }
-      if (end - n <= u0 && u0 < end) {
-        S.found = x;
-        S.before = end - n;
-      }
-      __syncthreads();
-      if (S.found >= 0) break;
-    }
-  }
+  const RunPlan pl = prefill_plan<PT_ROWS, PT_KEYS, PT_THREADS>(P, S.plan);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
@@ -431,18 +294,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // ------------------------------------------------------------ walk, queries --
     if (warp == 9) {
-      int xt = S.found, b = 0, nitem = 0, i = 0;          // i: tile of the unit looked up next
-      PtItem I = {};
-      long long ws = 0;                                   // weight before the row tile
-      auto run_of = [&](int i0) {                         // the row tile's tiles in this run; none: the run is over
-        const int nt = I.span.nA + I.span.nB;
-        I.i0 = i0;
-        I.i1 = (int)min((long long)nt, u1 - ws - PT_ITEM_WEIGHT);
-        I.elsewhere = (I.i0 > 0 ? 1 : 0) | (I.i1 < nt ? 2 : 0);
-        I.c0 = (int)((ws + PT_ITEM_WEIGHT) / per);
-        if (I.i1 <= I.i0) I.i1 = -1;
-        i = i0;
-      };
+      RowTileWalk<PT_ROWS, PT_KEYS> W(P, S.plan, pl);
+      const RowTile &I = W.I;
+      int nitem = 0, i = I.i0;                            // i: tile of the unit looked up next
       auto hand_over = [&]() {                            // the row tile, to the other warps
         const int e = nitem % PT_ITEMS;
         ok = ok && pt_wait(&S.iempty[e], ((nitem / PT_ITEMS) & 1) ^ 1);
@@ -452,22 +306,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         }
         ++nitem;
       };
-      auto enter = [&]() {                                // row tile xt
-        while (b + 1 < P.B && S.tiles[b + 1] <= xt) ++b;
-        pt_range(P, b, xt - S.tiles[b], I, 32);
-        if (lane == 0 && I.len < I.n) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
-      };
       if (lane == 0) P.rec[blockIdx.x * 8] = 0;
-      if (xt >= 0) {
-        b = seq_of(xt);
-        enter();
-        const int nt = I.span.nA + I.span.nB + PT_ITEM_WEIGHT;
-        I.kvh = (int)((u0 - S.before) / nt);
-        ws = S.before + (long long)I.kvh * nt;
-        run_of(max(0, (int)(u0 - ws) - PT_ITEM_WEIGHT));
-      } else {
-        I.i1 = -1;
-      }
       hand_over();
       // unit x is entered (its row tile handed over) and its page-table entries fetched while
       // unit x - 1's are turned into offsets
@@ -476,17 +315,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       uint32_t seen = 0, pseen = 0;                       // bit k: token t0 + lane + 32 k is seen by some row
       for (int x = 0;; ++x) {
         if (x > 0 && I.i1 >= 0 && i == I.i1) {
-          ws += I.span.nA + I.span.nB + PT_ITEM_WEIGHT;
-          if (I.kvh + 1 < Hkv) {
-            ++I.kvh;
-            run_of(0);
-          } else if (++xt < ntiles) {
-            I.kvh = 0;
-            enter();
-            run_of(0);
-          } else {
-            I.i1 = -1;
-          }
+          W.next();
+          i = I.i0;
           hand_over();
         }
         const bool more = I.i1 >= 0;
@@ -710,7 +540,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       const int e = nitem % PT_ITEMS;
       if (!pt_wait(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; break; }
       ++nitem;
-      const PtItem &I = S.item[e];
+      const RowTile &I = S.item[e];
       const int i0 = I.i0, i1 = I.i1;
       if (i1 < 0) break;
       if (t == 1 && I.nr <= 128) {
@@ -929,13 +759,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         else *reinterpret_cast<float2 *>(P.pml + prow * 2) = make_float2(m, l);
       }
       if (r == 0 && elsewhere == 1) {                      // a split row tile ends here: to be joined
-        int32_t *rec = P.rec + blockIdx.x * 8;
-        rec[1] = c0;
-        rec[2] = s0;
-        rec[3] = r0;
-        rec[4] = nr;
-        rec[5] = kvh;
-        rec[0] = 1;
+        join_record(P, c0, s0, r0, nr, kvh);
       }
     }
   }
@@ -947,43 +771,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
   if (S.fail && tid == 0) {
     P.rec[blockIdx.x * 8] = 0;
     paged_fail(C.status, ECHO_ERR_TIMEOUT);
-  }
-}
-
-// Joins the partials of the row tile that ends in CTA blockIdx.x, in the order of their units:
-// slot 1 of its first CTA, then slot 0 of the following ones.  A warp takes a row.
-template <int D>
-__global__ void __launch_bounds__(128) paged_prefill_join_kernel(const __grid_constant__ PrefillParams P) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c1 = blockIdx.x;
-  const int32_t *rec = P.rec + c1 * 8;
-  if (rec[0] == 0) return;
-  const int c0 = rec[1], s0 = rec[2], r0 = rec[3], nr = rec[4], kvh = rec[5];
-  const int lane = threadIdx.x & 31;
-  constexpr int VL = D / 32;
-  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < nr; r += gridDim.y * 4) {
-    float M = -INFINITY, L = 0.f, v[VL];
-#pragma unroll
-    for (int i = 0; i < VL; ++i) v[i] = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t row = (int64_t)(2 * c + (c == c0 ? 1 : 0)) * P.prows + r;
-      const float2 ml = *reinterpret_cast<const float2 *>(P.pml + row * 2);
-      const float nm = fmaxf(M, ml.x), z = nm == -INFINITY ? 0.f : nm;
-      const float wa = exp2f(M - z), wb = exp2f(ml.x - z);
-      M = nm;
-      L = L * wa + ml.y * wb;
-      const float *o = P.po + row * D + lane * VL;
-#pragma unroll
-      for (int i = 0; i < VL; ++i) v[i] = v[i] * wa + o[i] * wb;
-    }
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    const int tk = (r0 + r) / P.G, hd = kvh * P.G + (r0 + r) % P.G;
-    const int64_t orow = (int64_t)(s0 + tk) * P.Hq + hd;
-    __nv_bfloat16 *dst = (__nv_bfloat16 *)P.out + orow * D + lane * VL;
-#pragma unroll
-    for (int i = 0; i < VL; i += 2)
-      *reinterpret_cast<__nv_bfloat162 *>(dst + i) = __floats2bfloat162_rn(v[i] * inv, v[i + 1] * inv);
-    if (lane == 0) P.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPgLn2;
   }
 }
 
@@ -1037,10 +824,10 @@ static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
     const int qb[3] = {64, P.G, qbox};
     if (qbox && !bf16_map(&qmap, P.q, 3, qd, qs, qb)) qbox = 0;
   }
-  const int grid = std::min(sm_count(), PF_MAX_CTAS);
+  const int grid = std::min(sm_count(), PF_MAX_CTAS / 2);
   paged_prefill_tc_kernel<D, MOD><<<grid, PT_THREADS, pt_smem<D>(), st>>>(P, kmap, vmap, qmap, box, qbox);
   ECHO_LAUNCH_OK();
-  ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<D>, dim3(grid, std::max(1, std::min(16, P.prows / 16))), dim3(128), st, P));
+  ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<__nv_bfloat16, D>, dim3(grid, std::max(1, std::min(16, P.prows / 16))), dim3(128), st, P));
   return ECHO_OK;
 }
 
