@@ -15,7 +15,7 @@
 
 namespace echo {
 
-constexpr int PA_THREADS = 256;
+constexpr int PA_THREADS = 128;
 
 struct AppendParams {
   echo_paged_kv_t C;

@@ -8,8 +8,8 @@
 //
 // Split.  The cache is dealt out in units: tiles of TILE tokens of one KV head and up to ROWS
 // of its query heads, ordered by (sequence, KV head, tile).  A persistent grid computes from
-// the device's own lengths how many units there are and gives each CTA an equal run of them,
-// so that ragged batches, one long sequence and many short ones all spread evenly, and one
+// the device's own lengths how many units there are and gives each CTA a run of equal weight
+// (a (sequence, head) weighs one unit besides its tiles: its queries, its joining), so that ragged batches, one long sequence and many short ones all spread evenly, and one
 // captured graph serves any lengths.  A run may cross sequences; the loads run on across the
 // border.  A (sequence, head) whose units lie in one CTA is finished there; otherwise each of
 // its CTAs leaves a partial (o, m, l) -- at most two a CTA: the end of a run of units begun
@@ -31,9 +31,8 @@ namespace echo {
 constexpr int PD_THREADS = 128, PD_WARPS = 4;
 constexpr int PD_MAX_ROWS = 16;
 constexpr int PD_MAX_CTAS = 608;     // partial slots: two a CTA
-constexpr int PD_MIN_UNITS = 2;      // fewest units of a CTA's run
+constexpr int PD_MIN_WEIGHT = 3;     // least weight of a CTA's run
 constexpr int PD_RING = 8;           // units whose look-ups are kept
-constexpr int PD_STAGES = 3;
 
 struct DecodeParams {
   echo_paged_kv_t C;
@@ -63,6 +62,12 @@ struct PdShape {
   static constexpr int TILE = PD_WARPS * TW;
   static constexpr int ROWB = D * (int)sizeof(T);       // bytes of a key (or value)
   static constexpr int HALF = TW * ROWB;                // a warp's keys of a tile
+  // Stages of a warp's ring and CTAs an SM.  bf16 rows of 128 values stream best from two CTAs of
+  // three stages (16 x 32K-48K tokens: 396 us, two stages 401); d = 64 and float32 have more
+  // instructions a byte and want the warps of a third CTA (b96 capped 103 us, two CTAs 112; float32
+  // 39 us, two CTAs 43).
+  static constexpr int STAGES = BF && D == 128 ? 3 : 2;
+  static constexpr int CTAS = BF && D == 128 ? 2 : 3;
 };
 
 // What sequence b's query sees, as tiles; a sequence that sees nothing has one tile of
@@ -86,6 +91,7 @@ __device__ __forceinline__ DecodeSpan decode_span(const DecodeParams &P, int b, 
 // A unit of a warp's ring.
 struct UnitInfo {
   int b, hh, t0, len;                // t0: the warp's first token
+  int c0;                            // CTA of (b, hh)'s first unit
   int flags;                         // 1 the run's first unit of (b, hh), 2 its last, 4 begun elsewhere, 8 goes on elsewhere
   uint32_t there;                    // tokens that are seen and there
 };
@@ -94,9 +100,8 @@ template <typename T, int D>
 struct PdShared {
   using Sh = PdShape<T, D>;
   UnitInfo info[PD_WARPS][PD_RING];
-  long long sum[PD_WARPS];
+  uint32_t sum[PD_WARPS], before;    // before: weight before sequence seq
   int seq;
-  long long before;
   float m[PD_WARPS][PD_MAX_ROWS], l[PD_WARPS][PD_MAX_ROWS];
   alignas(16) float p[Sh::BF ? 1 : PD_WARPS][8][8];               // f32: weights [head][token]
 };
@@ -104,7 +109,7 @@ struct PdShared {
 template <typename T, int D>
 constexpr size_t pd_smem() {
   using Sh = PdShape<T, D>;
-  return 128 + (size_t)PD_WARPS * PD_STAGES * 2 * Sh::HALF + Sh::ROWS * Sh::ROWB + Sh::ROWS * D * 4 +
+  return 128 + (size_t)PD_WARPS * Sh::STAGES * 2 * Sh::HALF + Sh::ROWS * Sh::ROWB + (Sh::BF ? Sh::ROWS * D * 4 : 0) +
          sizeof(PdShared<T, D>);
 }
 
@@ -142,7 +147,8 @@ __device__ __forceinline__ uint32_t pd_at(int r, int c) {
 
 // One warp's attention state in bf16: 16 heads x D values as tensor-instruction accumulators
 // (rows gid and gid + 8 of the lane).
-template <int D>
+// R8: at most 8 heads, and nothing is done for rows gid + 8.
+template <int D, bool R8>
 struct WarpBf {
   using T = __nv_bfloat16;
   static constexpr int TW = PdShape<T, D>::TW, ROWB = PdShape<T, D>::ROWB;
@@ -157,7 +163,7 @@ struct WarpBf {
     const int gid = lane >> 2, mi = lane >> 3, r = (mi & 1) * 8 + (lane & 7);
     if (P.slopes) {
       if (gid < nrows) sl0 = P.slopes[h0 + gid] * kPgLog2e;
-      if (gid + 8 < nrows) sl1 = P.slopes[h0 + gid + 8] * kPgLog2e;
+      if (!R8 && gid + 8 < nrows) sl1 = P.slopes[h0 + gid + 8] * kPgLog2e;
     }
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) pd_ldsm_x4(smem_u32(qt) + pd_at<ROWB>(r, ks * 2 + (mi >> 1)), qa[ks]);
@@ -184,27 +190,28 @@ struct WarpBf {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int r = t * 8 + 2 * tig + y;
-        float a = score_log2(P.f, s[t][y]), c = score_log2(P.f, s[t][2 + y]);
-        if (P.slopes) {
-          const float far = (float)(I.len - 1 - (I.t0 + r));
-          a -= sl0 * far;
-          c -= sl1 * far;
-        }
+        const float far = (float)(I.len - 1 - (I.t0 + r));
         const bool ok = (I.there >> r) & 1u;
+        float a = score_log2(P.f, s[t][y]);
+        if (P.slopes) a -= sl0 * far;
         s[t][y] = ok ? a : -INFINITY;
-        s[t][2 + y] = ok ? c : -INFINITY;
         mx0 = fmaxf(mx0, s[t][y]);
-        mx1 = fmaxf(mx1, s[t][2 + y]);
+        if (!R8) {
+          float c = score_log2(P.f, s[t][2 + y]);
+          if (P.slopes) c -= sl1 * far;
+          s[t][2 + y] = ok ? c : -INFINITY;
+          mx1 = fmaxf(mx1, s[t][2 + y]);
+        }
       }
 #pragma unroll
     for (int y = 1; y <= 2; y <<= 1) {
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, y));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, y));
+      if (!R8) mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, y));
     }
     // a row's maximum moves a few times in a long sequence: the results are rescaled only then
-    if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
-      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-      const float c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), c1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+    if (__any_sync(0xffffffffu, mx0 > m0 || (!R8 && mx1 > m1))) {
+      const float n0 = fmaxf(m0, mx0), n1 = R8 ? m1 : fmaxf(m1, mx1);
+      const float c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), c1 = R8 || n1 == -INFINITY ? 1.f : ex2(m1 - n1);
       m0 = n0;
       m1 = n1;
       l0 *= c0;
@@ -213,8 +220,10 @@ struct WarpBf {
       for (int i = 0; i < D / 8; ++i) {
         o[i][0] *= c0;
         o[i][1] *= c0;
-        o[i][2] *= c1;
-        o[i][3] *= c1;
+        if (!R8) {
+          o[i][2] *= c1;
+          o[i][3] *= c1;
+        }
       }
     }
     const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
@@ -226,11 +235,15 @@ struct WarpBf {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const float *x = s[2 * g + t];
-        const float p0 = ex2(x[0] - z0), p1 = ex2(x[1] - z0), p2 = ex2(x[2] - z1), p3 = ex2(x[3] - z1);
+        const float p0 = ex2(x[0] - z0), p1 = ex2(x[1] - z0);
         l0 += p0 + p1;
-        l1 += p2 + p3;
         pa[2 * t] = pd_pack(p0, p1);
-        pa[2 * t + 1] = pd_pack(p2, p3);
+        pa[2 * t + 1] = 0;
+        if (!R8) {
+          const float p2 = ex2(x[2] - z1), p3 = ex2(x[3] - z1);
+          l1 += p2 + p3;
+          pa[2 * t + 1] = pd_pack(p2, p3);
+        }
       }
       const int r = g * 16 + (mi & 1) * 8 + (lane & 7);
 #pragma unroll
@@ -267,11 +280,17 @@ struct WarpBf {
       float2 *a = reinterpret_cast<float2 *>(acc + gid * D + i * 8 + col), *c = reinterpret_cast<float2 *>(acc + (gid + 8) * D + i * 8 + col);
       float2 x = make_float2(o[i][0] * f0, o[i][1] * f0), y = make_float2(o[i][2] * f1, o[i][3] * f1);
       if (!set) {
-        const float2 u = *a, v = *c;
-        x.x += u.x; x.y += u.y; y.x += v.x; y.y += v.y;
+        const float2 u = *a;
+        x.x += u.x; x.y += u.y;
       }
       *a = x;
-      *c = y;
+      if (!R8) {
+        if (!set) {
+          const float2 v = *c;
+          y.x += v.x; y.y += v.y;
+        }
+        *c = y;
+      }
     }
   }
 };
@@ -395,97 +414,79 @@ struct WarpF32 {
   }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const __grid_constant__ DecodeParams P) {
+template <typename T, int D, bool R8>
+__global__ void __launch_bounds__(PD_THREADS, PdShape<T, D>::CTAS) paged_decode_kernel(const __grid_constant__ DecodeParams P) {
   using Sh = PdShape<T, D>;
-  using State = std::conditional_t<Sh::BF, WarpBf<D>, WarpF32<D>>;
-  constexpr int TILE = Sh::TILE, TW = Sh::TW, ST = PD_STAGES, ROWB = Sh::ROWB, HALF = Sh::HALF, ROWS = Sh::ROWS;
+  using State = std::conditional_t<Sh::BF, WarpBf<D, R8>, WarpF32<D>>;
+  constexpr int TILE = Sh::TILE, TW = Sh::TW, ST = Sh::STAGES, ROWB = Sh::ROWB, HALF = Sh::HALF, ROWS = Sh::ROWS;
   constexpr int KC = ROWB / 16;                          // 16-byte chunks of a key
   extern __shared__ unsigned char pd_raw[];
   unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(pd_raw) + 127) & ~uintptr_t(127));
   unsigned char *qs = sm + PD_WARPS * ST * 2 * HALF;     // the query tile
-  float *acc = reinterpret_cast<float *>(qs + ROWS * ROWB);                // the warps' results, joined
-  PdShared<T, D> &S = *reinterpret_cast<PdShared<T, D> *>(acc + ROWS * D);
+  float *acc = reinterpret_cast<float *>(qs + (Sh::BF ? ROWS * ROWB : 0));                // the warps' results, joined
+  PdShared<T, D> &S = *reinterpret_cast<PdShared<T, D> *>(qs + ROWS * ROWB + (Sh::BF ? ROWS * D * 4 : 0));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const echo_paged_kv_t &C = P.C;
   const int HH = C.n_kv_heads * P.HG;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's run of units: a scan over the sequences, PD_THREADS at a time; with few
-  // sequences one scan gives the total and finds the place
-  long long total = 0, end = 0, n = 0;
-  if (tid == 0) S.seq = -1;
-  for (int b0 = 0; b0 < P.B; b0 += PD_THREADS) {
-    n = b0 + tid < P.B ? (long long)decode_span(P, b0 + tid, TILE).n() * HH : 0;
-    long long x = n;
+  // ---- this CTA's run: a scan over the sequences, PD_THREADS at a time; with few sequences one
+  // scan gives the total and finds the place
+  uint32_t total = 0, end = 0, n = 0, per = 0, u0 = 0, u1 = 0;
+  if (tid == 0) { S.seq = -1; P.rec[blockIdx.x * 4] = 0; }
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t at = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < P.B && (pass == 0 || S.seq < 0); b0 += PD_THREADS) {
+      if (pass == 0 || P.B > PD_THREADS) {
+        n = b0 + tid < P.B ? (uint32_t)(decode_span(P, b0 + tid, TILE).n() + 1) * (uint32_t)HH : 0;
+        uint32_t x = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) S.sum[warp] = x;
-    __syncthreads();
-    end = total + x;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) S.sum[warp] = x;
+        __syncthreads();
+        end = at + x;
 #pragma unroll
-    for (int w = 0; w < PD_WARPS; ++w) {
-      if (w < warp) end += S.sum[w];
-      total += S.sum[w];
-    }
-  }
-  const long long per = max(total <= 0x7fffffff ? (long long)(((unsigned)total + P.nctas - 1) / (unsigned)P.nctas)
-                                                : (total + P.nctas - 1) / P.nctas, (long long)PD_MIN_UNITS);
-  const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
-  if (tid == 0) P.rec[blockIdx.x * 4] = 0;
-  if (u0 >= u1) return;
-  if (P.B <= PD_THREADS) {
-    if (end - n <= u0 && u0 < end) { S.seq = tid; S.before = end - n; }
-    __syncthreads();
-  } else {
-    long long base = 0;
-    for (int b0 = 0; b0 < P.B; b0 += PD_THREADS) {
-      n = b0 + tid < P.B ? (long long)decode_span(P, b0 + tid, TILE).n() * HH : 0;
-      long long x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        for (int w = 0; w < PD_WARPS; ++w) {
+          if (w < warp) end += S.sum[w];
+          at += S.sum[w];
+        }
       }
-      __syncthreads();
-      if (lane == 31) S.sum[warp] = x;
-      __syncthreads();
-      end = base + x;
-#pragma unroll
-      for (int w = 0; w < PD_WARPS; ++w) {
-        if (w < warp) end += S.sum[w];
-        base += S.sum[w];
+      if (pass == 1) {
+        if (end - n <= u0 && u0 < end) { S.seq = b0 + tid; S.before = end - n; }
+        __syncthreads();
       }
-      if (end - n <= u0 && u0 < end) { S.seq = b0 + tid; S.before = end - n; }
-      __syncthreads();
-      if (S.seq >= 0) break;
+    }
+    if (pass == 0) {
+      total = at;
+      per = max((total + P.nctas - 1) / P.nctas, (uint32_t)PD_MIN_WEIGHT);
+      u0 = per * blockIdx.x;
+      u1 = min(total, u0 + per);
+      if (u0 >= total) return;
     }
   }
 
-  // ---- cursor of the look-ups (the same in every thread)
+  // ---- cursor of the look-ups (the same in every thread): tile ci of its part [i0, ce) of the
+  // current (sequence, head group), which begins at weight ws
   int cb = S.seq;
   DecodeSpan cs = decode_span(P, cb, TILE);
-  int chh, ci;
-  {
-    const long long off = u0 - S.before;                 // below 2^31 tiles times heads of one sequence
-    const int cn = cs.n();
-    chh = off <= 0x7fffffff ? (int)((unsigned)off / (unsigned)cn) : (int)(off / cn);
-    ci = (int)(off - (long long)chh * cn);
-  }
-  const int c0 = (int)((u0 - ci) / per);                 // CTA in which the first (sequence, head group) begins
-  const int nu = (int)(u1 - u0);
+  int cn = cs.n(), chh = (int)((u0 - S.before) / (uint32_t)(cn + 1)), ci, i0, ce;
+  uint32_t ws = S.before + (uint32_t)chh * (uint32_t)(cn + 1);
+  i0 = ci = max(0, (int)(u0 - ws) - 1);
+  ce = min(cn, (int)(u1 - ws) - 1);
   int cu = 0;                                            // units looked up
   int32_t ent = -1;                                      // the last one's page-table entry of this lane's token
   int tok = -1;
   UnitInfo *ring = S.info[warp];
   auto look_up = [&]() {
     tok = -1;
-    if (cu >= nu) return;
-    const int cn = cs.n(), t0 = cs.t.tile(ci) * TILE + warp * TW;
+    if (ci >= ce) return;                                // the run is over
+    const int t0 = cs.t.tile(ci) * TILE + warp * TW;
     const int t = t0 + lane;
     if (lane < TW && t >= cs.first && t < cs.len && (t >= cs.lo || t < cs.pre)) {
       tok = t;
@@ -493,23 +494,30 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const __grid_c
     }
     if (lane == 0) {
       UnitInfo &I = ring[cu % PD_RING];
-      const bool last = ci + 1 == cn || cu + 1 == nu;
       I.b = cb; I.hh = chh; I.t0 = t0; I.len = cs.len;
-      I.flags = ((ci == 0 || cu == 0) ? 1 : 0) | (last ? 2 : 0) | (cu < ci ? 4 : 0) | (last && ci + 1 != cn ? 8 : 0);
+      I.flags = (ci == i0 ? 1 : 0) | (ci + 1 == ce ? 2 : 0) | (i0 > 0 ? 4 : 0) | (ce < cn ? 8 : 0);
+      I.c0 = (int)((ws + 1) / per);
     }
     ++cu;
-    if (++ci == cn) {
-      ci = 0;
+    if (++ci == ce && ce == cn) {                        // on to the next (sequence, head group)
+      ws += cn + 1;
       if (++chh == HH) {
         chh = 0;
-        if (cu < nu && cb + 1 < P.B) cs = decode_span(P, ++cb, TILE);
+        if (cb + 1 < P.B) {
+          cs = decode_span(P, ++cb, TILE);
+          cn = cs.n();
+        } else {
+          ws = u1;
+        }
       }
+      i0 = ci = 0;
+      ce = min(cn, (int)(u1 - ws) - 1);
     }
   };
   // turns unit x's entries into offsets and copies the warp's keys and values into its stage
   unsigned char *stages = sm + warp * ST * 2 * HALF;
   auto load = [&](int x) {
-    if (x < nu) {
+    if (x < cu) {
       int64_t row = -1;
       if (tok >= 0) {
         if (ent < 0 || ent >= C.n_pages) paged_fail(C.status, ECHO_ERR_PAGE);
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const __grid_c
 
   State A;
   int nrows = 0, h0 = 0;
-  for (int x = 0; x < nu; ++x) {
+  for (int x = 0; x < cu; ++x) {                         // (the look-ups are ahead of it, or over)
     cp_async_wait<ST - 2>();
     __syncwarp();                                        // unit x is there, and unit x - 1's stage is free
     load(x + ST - 1);
@@ -552,6 +560,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const __grid_c
       const int hg = I.hh % P.HG;
       h0 = (I.hh / P.HG) * P.G + hg * ROWS;
       nrows = min(ROWS, P.G - hg * ROWS);
+      if (!Sh::BF) __syncthreads();                      // float32's joined results lie in the query tile's place
       const T *q = (const T *)P.q + (int64_t)I.b * P.q_stride + (int64_t)h0 * D;
       for (int i = tid; i < ROWS * KC; i += PD_THREADS) {
         const int r = i / KC, c = i % KC;
@@ -604,7 +613,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_kernel(const __grid_c
       }
       if (tid == 0 && (I.flags & 12) == 4) {             // a split one ends here: to be joined
         int32_t *rec = P.rec + blockIdx.x * 4;
-        rec[1] = c0;
+        rec[1] = I.c0;
         rec[2] = I.b;
         rec[3] = I.hh;
         rec[0] = 1;
@@ -662,19 +671,28 @@ __global__ void __launch_bounds__(D) paged_decode_join_kernel(const __grid_const
   if (tid == 0) P.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kPgLn2;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool R8>
 static echo_status_t launch_decode(DecodeParams &P, cudaStream_t st) {
+  using Sh = PdShape<T, D>;
   constexpr size_t smem = pd_smem<T, D>();
-  constexpr int occ = (int)std::min<size_t>(4, 227 * 1024 / (smem + 1024));
-  static_assert(occ >= 2, "two CTAs an SM hide one another's latencies");
-  P.HG = (P.G + PdShape<T, D>::ROWS - 1) / PdShape<T, D>::ROWS;
-  P.prows = std::min(P.G, PdShape<T, D>::ROWS);
-  P.nctas = std::min(sm_count() * occ, PD_MAX_CTAS);
-  ECHO_CUDA_OK((allow_smem<paged_decode_kernel<T, D>>(smem)));
-  paged_decode_kernel<T, D><<<P.nctas, PD_THREADS, smem, st>>>(P);
+  static_assert(Sh::CTAS * (smem + 1024) <= 228 * 1024, "the CTAs of an SM fit its shared memory");
+  P.HG = (P.G + Sh::ROWS - 1) / Sh::ROWS;
+  P.prows = std::min(P.G, Sh::ROWS);
+  P.nctas = std::min(sm_count() * Sh::CTAS, PD_MAX_CTAS);
+  // weights are counted in 32 bits: sequences x heads x tiles of the longest one
+  if ((double)P.B * P.C.n_kv_heads * P.HG * ((double)P.C.max_pages * P.C.page_tokens / Sh::TILE + 4) > 2147483647.0)
+    return ECHO_ERR_UNSUPPORTED;
+  ECHO_CUDA_OK((allow_smem<paged_decode_kernel<T, D, R8>>(smem)));
+  paged_decode_kernel<T, D, R8><<<P.nctas, PD_THREADS, smem, st>>>(P);
   ECHO_LAUNCH_OK();
   ECHO_CUDA_OK(launch_after(paged_decode_join_kernel<T, D>, dim3(P.nctas, P.prows), dim3(D), st, P));
   return ECHO_OK;
+}
+
+template <int D>
+static echo_status_t launch_decode_d(DecodeParams &P, cudaStream_t st) {
+  if (P.C.dtype == ECHO_F32) return launch_decode<float, D, true>(P, st);
+  return P.G <= 8 ? launch_decode<__nv_bfloat16, D, true>(P, st) : launch_decode<__nv_bfloat16, D, false>(P, st);
 }
 
 }  // namespace echo
@@ -714,7 +732,5 @@ extern "C" echo_status_t echo_paged_attn_decode(const echo_paged_kv_t *cache, co
   P.po = reinterpret_cast<float *>(P.rec + 4 * PD_MAX_CTAS);
   P.pml = P.po + (size_t)2 * PD_MAX_CTAS * std::min(P.G, PD_MAX_ROWS) * cache->head_dim;
   cudaStream_t cs = (cudaStream_t)stream;
-  if (cache->dtype == ECHO_BF16)
-    return cache->head_dim == 128 ? launch_decode<__nv_bfloat16, 128>(P, cs) : launch_decode<__nv_bfloat16, 64>(P, cs);
-  return cache->head_dim == 128 ? launch_decode<float, 128>(P, cs) : launch_decode<float, 64>(P, cs);
+  return cache->head_dim == 128 ? launch_decode_d<128>(P, cs) : launch_decode_d<64>(P, cs);
 }

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(PS_THREADS, 2) paged_prefill_simt_kernel(const
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int G = P.G;
   if (tid == 0) P.rec[blockIdx.x * 8] = 0;
-  const RunPlan pl = prefill_plan<PS_ROWS, PS_KEYS, PS_THREADS>(P, S.plan);
+  const RunPlan pl = prefill_plan<PS_ROWS, PS_KEYS, PS_THREADS>(P, S.plan, reinterpret_cast<uint32_t *>(ps_sm));
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   for (RowTileWalk<PS_ROWS, PS_KEYS> W(P, S.plan, pl); W.I.i1 >= 0; W.next()) {
@@ -261,6 +261,10 @@ extern "C" echo_status_t echo_paged_attn_prefill(const echo_paged_kv_t *cache, c
   cudaStream_t cs = (cudaStream_t)stream;
   const bool bf = cache->dtype == ECHO_BF16;
   P.prows = prefill_prows(N, P.G, bf ? PF_MAX_ROWS : PS_ROWS);
+  // the units are counted in 32 bits: row tiles x (tiles of the longest sequence) x KV heads
+  const double tiles = (double)N * P.G / (bf ? PF_MAX_ROWS : PS_ROWS) + B;
+  const double deep = (double)cache->max_pages * cache->page_tokens / (bf ? 2 * PS_KEYS : PS_KEYS) + 4;
+  if (tiles * deep * cache->n_kv_heads > 2147483647.0) return ECHO_ERR_UNSUPPORTED;
   P.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   P.rec = reinterpret_cast<int32_t *>(workspace);
   P.po = reinterpret_cast<float *>(P.rec + 8 * PF_MAX_CTAS);

@@ -50,8 +50,8 @@ struct RowTile {
   int c0;                            // CTA of its first unit
 };
 
-// What the rows of row tile rt of sequence b see.  Lanes of a warp share the rows when
-// `lanes` is 32 (all of them call); one thread walks them alone when it is 1.
+// What the rows of row tile rt of sequence b see.  Groups of `lanes` lanes (1, 8 or 32) share the
+// rows of a tile; with more than one, every lane of the warp calls.
 template <int ROWS, int KEYS>
 __device__ __forceinline__ void row_tile_range(const PrefillParams &P, int b, int rt, RowTile &I, int lanes) {
   const SeqRows R = seq_rows(P, b);
@@ -72,18 +72,27 @@ __device__ __forceinline__ void row_tile_range(const PrefillParams &P, int b, in
     I.pre = 0;
   } else if (P.first_tok) {
     first = lo = 0x7fffffff;
-    for (int i = i0 + (lanes > 1 ? (int)(threadIdx.x & 31) : 0); i <= i1; i += lanes) {
-      const int f = max(__ldg(P.first_tok + R.s0 + i), 0);
-      first = min(first, f);
-      lo = min(lo, P.window ? max(f, p0 + i - P.window + 1) : f);
+    for (int i = i0 + ((int)threadIdx.x & (lanes - 1)); i <= i1; i += 8 * lanes) {
+      int f[8];                                           // eight loads under way at a time
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = i + k * lanes <= i1 ? __ldg(P.first_tok + R.s0 + i + k * lanes) : 0x7fffffff;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int g = max(f[k], 0);
+        first = min(first, g);
+        lo = min(lo, P.window ? max(g, p0 + i + k * lanes - P.window + 1) : g);
+      }
     }
-    if (lanes > 1) {
-      first = __reduce_min_sync(0xffffffffu, first);
-      lo = __reduce_min_sync(0xffffffffu, lo);
-    }
-  } else if (P.window) {
-    lo = max(0, p0 + i0 - P.window + 1);
   }
+  if (P.first_tok && lanes > 1) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < lanes) {
+        first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      }
+  }
+  if (!P.first_tok && i1 >= i0 && P.window) lo = max(0, p0 + i0 - P.window + 1);
   I.first = first;
   I.lo = lo;
   I.hi = i1 < i0 ? 0 : p0 + i1 + 1;
@@ -96,13 +105,13 @@ __device__ __forceinline__ void row_tile_range(const PrefillParams &P, int b, in
 // PF_ITEM_WEIGHT units' worth of weight (its queries, its epilogue).  CTA c gets the weights
 // [per c, per (c + 1)): a tile belongs to the CTA that holds its last one.
 struct PlanShared {
-  long long sum[32];
-  long long before;                  // weight before row tile `found`
+  uint32_t sum[32];
+  uint32_t before;                   // weight before row tile `found`
   int found;                         // row tile in which the run begins, -1: no run
   int tiles[PF_MAX_B + 1];           // row tiles before each sequence
 };
 struct RunPlan {
-  long long per, u0, u1;
+  uint32_t per, u0, u1;              // below 2^31: the call refuses more
   int ntiles;
 };
 // Last sequence whose row tiles begin at or before x.
@@ -116,72 +125,86 @@ __device__ __forceinline__ int plan_seq(const PlanShared &S, int B, int x) {
 }
 // Inclusive sum over the block of v, and the block's total; the whole block calls it.
 template <int THREADS>
-__device__ __forceinline__ long long plan_scan(PlanShared &S, long long v, long long &total) {
+__device__ __forceinline__ uint32_t plan_scan(PlanShared &S, uint32_t v, uint32_t &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += y;
   }
   __syncthreads();
   if (lane == 31) S.sum[warp] = v;
   __syncthreads();
-  total = 0;
-#pragma unroll 4
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) v += S.sum[w];
-    total += S.sum[w];
-  }
-  return v;
+  const uint32_t w = lane < THREADS / 32 ? S.sum[lane] : 0;
+  total = __reduce_add_sync(0xffffffffu, w);
+  return v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
 }
+// `wt`: shared memory for the weights of PLAN_TILES row tiles, free again when the call ends.
+constexpr int PLAN_TILES = 8192;
 template <int ROWS, int KEYS, int THREADS>
-__device__ __forceinline__ RunPlan prefill_plan(const PrefillParams &P, PlanShared &S) {
+__device__ __forceinline__ RunPlan prefill_plan(const PrefillParams &P, PlanShared &S, uint32_t *wt) {
   const int tid = threadIdx.x;
   RunPlan pl;
   if (tid == 0) S.found = -1;
-  long long base = 0, sum;
+  uint32_t base = 0, sum;
+#pragma unroll 1
   for (int b0 = 0; b0 < P.B; b0 += THREADS) {
     const int b = b0 + tid;
-    const long long n = b < P.B ? ((int64_t)seq_rows(P, b).n * P.G + ROWS - 1) / ROWS : 0;
-    const long long end = base + plan_scan<THREADS>(S, n, sum);
+    const uint32_t n = b < P.B ? (uint32_t)(((int64_t)seq_rows(P, b).n * P.G + ROWS - 1) / ROWS) : 0;
+    const uint32_t end = base + plan_scan<THREADS>(S, n, sum);
     if (b < P.B) S.tiles[b] = (int)(end - n);
     base += sum;
   }
   if (tid == 0) S.tiles[P.B] = (int)base;
   pl.ntiles = (int)base;
   __syncthreads();
-  // two passes over the row tiles: the total, then the one that holds the CTA's first weight
-  long long total = 0, n = 0;
+  // PLAN_TILES row tiles at a time: their weights, then a scan in which a thread takes a run of
+  // them.  The first pass gives the total, the second (the same values, where they all fit) the
+  // row tile that holds the CTA's first weight.  First tokens are read by eight lanes a tile.
+  const int grp = P.first_tok ? 8 : 1;
   pl.per = pl.u0 = pl.u1 = 0;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    long long at = 0;
-    for (int x0 = 0; x0 < pl.ntiles; x0 += THREADS) {
-      const int x = x0 + tid;
-      if (pass == 0 || pl.ntiles > THREADS) {             // few row tiles: the first pass's values still hold
-        n = 0;
-        if (x < pl.ntiles) {
+    uint32_t at = 0;
+#pragma unroll 1
+    for (int x0 = 0; x0 < pl.ntiles; x0 += PLAN_TILES) {
+      const int nx = min(PLAN_TILES, pl.ntiles - x0);
+      if (pass == 0 || pl.ntiles > PLAN_TILES) {
+        __syncthreads();
+#pragma unroll 1
+        for (int i = tid / grp; i < ((nx + 31) & ~31); i += THREADS / grp) {
           RowTile I;
-          const int b = plan_seq(S, P.B, x);
-          row_tile_range<ROWS, KEYS>(P, b, x - S.tiles[b], I, 1);
-          n = (long long)(I.span.nA + I.span.nB + PF_ITEM_WEIGHT) * P.C.n_kv_heads;
+          const int x = x0 + min(i, nx - 1), b = plan_seq(S, P.B, x);
+          row_tile_range<ROWS, KEYS>(P, b, x - S.tiles[b], I, grp);
+          if (i < nx && (tid & (grp - 1)) == 0)
+            wt[i] = (uint32_t)(I.span.nA + I.span.nB + PF_ITEM_WEIGHT) * (uint32_t)P.C.n_kv_heads;
         }
+        __syncthreads();
       }
-      const long long end = at + plan_scan<THREADS>(S, n, sum);
+      const int c = (nx + THREADS - 1) / THREADS, i0 = min(tid * c, nx), i1 = min(i0 + c, nx);
+      uint32_t n = 0;
+      for (int i = i0; i < i1; ++i) n += wt[i];
+      uint32_t end = at + plan_scan<THREADS>(S, n, sum);
       at += sum;
-      if (pass == 1 && end - n <= pl.u0 && pl.u0 < end) {
-        S.found = x;
-        S.before = end - n;
+      if (pass == 1) {
+        if (end - n <= pl.u0 && pl.u0 < end) {
+          uint32_t u = end - n;
+          int i = i0;
+          while (u + wt[i] <= pl.u0) u += wt[i++];
+          S.found = x0 + i;
+          S.before = u;
+        }
+        if (pl.u0 < at) break;                            // the same in every thread
       }
-      if (pass == 1 && pl.u0 < at) break;                 // the same in every thread
     }
     if (pass == 0) {
-      total = at;
-      pl.per = max((total + gridDim.x - 1) / (long long)gridDim.x, 1ll);
+      pl.per = max((at + gridDim.x - 1) / gridDim.x, 1u);
       pl.u0 = pl.per * blockIdx.x;
-      pl.u1 = min(total, pl.u0 + pl.per);
-      if (pl.u0 >= total) break;
+      pl.u1 = min(at, pl.u0 + pl.per);
+      if (pl.u0 >= at) break;
     }
   }
+  fence_proxy_async_smem();                               // the loads take wt's place
   __syncthreads();
   return pl;
 }
@@ -194,7 +217,7 @@ struct RowTileWalk {
   const RunPlan pl;
   RowTile I;
   int xt, b;
-  long long ws;                      // weight before the row tile
+  uint32_t ws;                       // weight before the row tile
 
   __device__ __forceinline__ void enter() {
     while (b + 1 < P.B && S.tiles[b + 1] <= xt) ++b;
@@ -204,7 +227,7 @@ struct RowTileWalk {
   __device__ __forceinline__ void part(int i0) {          // its tiles in this run; none: the run is over
     const int nt = I.span.nA + I.span.nB;
     I.i0 = i0;
-    I.i1 = (int)min((long long)nt, pl.u1 - ws - PF_ITEM_WEIGHT);
+    I.i1 = min(nt, (int)(pl.u1 - ws) - PF_ITEM_WEIGHT);
     I.elsewhere = (I.i0 > 0 ? 1 : 0) | (I.i1 < nt ? 2 : 0);
     I.c0 = (int)((ws + PF_ITEM_WEIGHT) / pl.per);
     if (I.i1 <= I.i0) I.i1 = -1;
@@ -217,7 +240,7 @@ struct RowTileWalk {
     enter();
     const int nt = I.span.nA + I.span.nB + PF_ITEM_WEIGHT;
     I.kvh = (int)((pl.u0 - S.before) / nt);
-    ws = S.before + (long long)I.kvh * nt;
+    ws = S.before + (uint32_t)I.kvh * nt;
     part(max(0, (int)(pl.u0 - ws) - PF_ITEM_WEIGHT));
   }
   __device__ __forceinline__ void next() {

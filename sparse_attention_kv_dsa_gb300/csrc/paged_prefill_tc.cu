@@ -227,8 +227,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     tmem_alloc(&S.tmem_base, 512);
     tmem_relinquish();
   }
+  if (tid == 32) {                                        // the first loads' descriptors, on their way
+    if (box) {
+      tma_prefetch_desc(&kmap);
+      tma_prefetch_desc(&vmap);
+    }
+    if (qbox) tma_prefetch_desc(&qmap);
+  }
 
-  const RunPlan pl = prefill_plan<PT_ROWS, PT_KEYS, PT_THREADS>(P, S.plan);
+  const RunPlan pl = prefill_plan<PT_ROWS, PT_KEYS, PT_THREADS>(P, S.plan, reinterpret_cast<uint32_t *>(R));
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
