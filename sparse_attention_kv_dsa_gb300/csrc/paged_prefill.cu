@@ -215,7 +215,7 @@ static echo_status_t launch_simt(const PrefillParams &P, cudaStream_t st) {
   const int grid = std::min(2 * sm_count(), PF_MAX_CTAS);
   paged_prefill_simt_kernel<D><<<grid, PS_THREADS, ps_smem<D>(), st>>>(P);
   ECHO_LAUNCH_OK();
-  ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<float, D>, dim3(grid, std::max(1, P.prows / 16)), dim3(128), st, P));
+  ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<float, D>, dim3(grid, (P.prows + 3) / 4), dim3(128), st, P));
   return ECHO_OK;
 }
 
