@@ -80,8 +80,9 @@ __device__ __forceinline__ int64_t paged_row(const echo_paged_kv_t &C, int b, in
 // Scores in base-2 units: log2(e) * x of a raw product s = q . k.
 //   no cap:  s * a             with a = scale log2(e)
 //   cap:     c tanh(s a)       with a = scale / cap, c = cap log2(e)
-// tanh(u) = 1 - 2 / (2^(2 u log2 e) + 1): its error stays near 1e-7 (absolute), so a score
-// is off by about 1e-7 of the cap, where the approximate tanh instruction is off by 5e-4.
+// tanh(u) is a polynomial for small u (a few roundings of u itself) and else
+// 1 - 2 / (2^(2 u log2 e) + 1), off by some 1e-7, where the approximate tanh instruction is off
+// by 5e-4 of the cap.
 struct ScoreForm {
   float a, c;
   int capped;
@@ -100,15 +101,20 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 __device__ __forceinline__ float tanh_ex2(float u) { return 1.f - __fdividef(2.f, ex2(2.f * kPgLog2e * u) + 1.f); }
-__device__ __forceinline__ float score_log2(const ScoreForm &f, float s) {
-  const float u = s * f.a;
-  return f.capped ? f.c * tanh_ex2(u) : u;
-}
 // tanh(u) = u (1 + w (c1 + w (c2 + ...))), w = u^2 <= 1/2: minimax in relative error, found by an
 // exchange of extrema; 1.5e-8 off.
 constexpr float kTanhW = 0.5f;
 constexpr float kTanh1 = -0.3333311080932617f, kTanh2 = 0.13328056037425995f, kTanh3 = -0.05350292846560478f,
                 kTanh4 = 0.01996474526822567f, kTanh5 = -0.005034889094531536f;
+__device__ __forceinline__ float score_tanh(float u) {
+  const float w = u * u;
+  if (!(w <= kTanhW)) return tanh_ex2(u);
+  return fmaf(u * w, fmaf(w, fmaf(w, fmaf(w, fmaf(w, kTanh5, kTanh4), kTanh3), kTanh2), kTanh1), u);
+}
+__device__ __forceinline__ float score_log2(const ScoreForm &f, float s) {
+  const float u = s * f.a;
+  return f.capped ? f.c * score_tanh(u) : u;
+}
 
 // Allows kernel K its dynamic shared memory: once for each device, not with every launch (the
 // call costs several microseconds of host time).
