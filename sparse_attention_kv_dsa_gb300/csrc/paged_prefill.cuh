@@ -160,8 +160,11 @@ __device__ __forceinline__ RunPlan prefill_plan(const PrefillParams &P, PlanShar
   __syncthreads();
   // PLAN_TILES row tiles at a time: their weights, then a scan in which a thread takes a run of
   // them.  The first pass gives the total, the second (the same values, where they all fit) the
-  // row tile that holds the CTA's first weight.  First tokens are read by eight lanes a tile.
-  const int grp = P.first_tok ? 8 : 1;
+  // row tile that holds the CTA's first weight.  First tokens are read by up to eight lanes a
+  // tile, as many as there are threads for.
+  int grp = 1;
+  while (P.first_tok && grp < 8 && 2 * grp * pl.ntiles <= THREADS) grp *= 2;
+  uint32_t n = 0, end = 0;
   pl.per = pl.u0 = pl.u1 = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
@@ -182,9 +185,11 @@ __device__ __forceinline__ RunPlan prefill_plan(const PrefillParams &P, PlanShar
         __syncthreads();
       }
       const int c = (nx + THREADS - 1) / THREADS, i0 = min(tid * c, nx), i1 = min(i0 + c, nx);
-      uint32_t n = 0;
-      for (int i = i0; i < i1; ++i) n += wt[i];
-      uint32_t end = at + plan_scan<THREADS>(S, n, sum);
+      if (pass == 0 || pl.ntiles > PLAN_TILES) {
+        n = 0;
+        for (int i = i0; i < i1; ++i) n += wt[i];
+        end = at + plan_scan<THREADS>(S, n, sum);
+      }
       at += sum;
       if (pass == 1) {
         if (end - n <= pl.u0 && pl.u0 < end) {

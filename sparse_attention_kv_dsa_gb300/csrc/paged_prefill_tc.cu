@@ -318,25 +318,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       };
       if (lane == 0) P.rec[blockIdx.x * 8] = 0;
       hand_over();
-      // unit x is entered (its row tile handed over) and its page-table entries fetched while
-      // unit x - 1's are turned into offsets
-      int32_t ent[4] = {-1, -1, -1, -1}, pent[4];
-      int t0 = 0, pt0 = 0, pkvh = -1;
-      uint32_t seen = 0, pseen = 0;                       // bit k: token t0 + lane + 32 k is seen by some row
       for (int x = 0;; ++x) {
-        if (x > 0 && I.i1 >= 0 && i == I.i1) {
+        if (x > 0 && i == I.i1) {
           W.next();
           i = I.i0;
           hand_over();
         }
         const bool more = I.i1 >= 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) pent[k] = ent[k];
-        pt0 = t0;
-        pseen = seen;
+        const int e = x % PT_UNITS, v = x % PT_VM, t0 = more ? I.span.tile(i++) * PT_KEYS : 0;
+        int32_t ent[4];
+        uint32_t seen = 0, all = 0xffffffffu;             // seen, bit k: token t0 + lane + 32 k is seen by some row
         if (more) {
-          t0 = I.span.tile(i) * PT_KEYS;
-          seen = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int t = t0 + lane + 32 * k;
@@ -344,47 +336,41 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
             seen |= some ? 1u << k : 0u;
             ent[k] = some ? __ldg(C.page_table + (int64_t)I.b * C.max_pages + div_by(P.page, t)) : -1;
           }
-          ++i;
         }
-        if (x > 0) {                                      // unit x - 1
-          const int e = (x - 1) % PT_UNITS, v = (x - 1) % PT_VM;
-          ok = ok && pt_wait(&S.uempty[e], (((x - 1) / PT_UNITS) & 1) ^ 1);
-          if (!ok) break;                                 // the others give up at their own waits
-          if (pkvh >= 0) {
-            uint32_t all = 0xffffffffu;
+        ok = ok && pt_wait(&S.uempty[e], ((x / PT_UNITS) & 1) ^ 1);
+        if (!ok) break;                                   // the others give up at their own waits
+        if (more) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const bool page = ent[k] >= 0 && ent[k] < C.n_pages;
+            if (((seen >> k) & 1u) && !page) paged_fail(C.status, ECHO_ERR_PAGE);
+            const uint32_t m = __ballot_sync(0xffffffffu, page);
+            all &= m;
+            if (lane == 0) S.vm[v][k] = m;
+            S.page[e][lane + 32 * k] = ent[k];
+          }
+          if (!box || all != 0xffffffffu) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const bool page = pent[k] >= 0 && pent[k] < C.n_pages;
-              if (((pseen >> k) & 1u) && !page) paged_fail(C.status, ECHO_ERR_PAGE);
-              const uint32_t m = __ballot_sync(0xffffffffu, page);
-              all &= m;
-              if (lane == 0) S.vm[v][k] = m;
-              S.page[e][lane + 32 * k] = pent[k];
-            }
-            if (!box || all != 0xffffffffu) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int t = pt0 + lane + 32 * k;
-                const bool page = pent[k] >= 0 && pent[k] < C.n_pages;
-                S.row[e][lane + 32 * k] = page ? (int64_t)pent[k] * C.page_stride +
-                                                     (int64_t)(t - div_by(P.page, t) * C.page_tokens) * C.row_stride
-                                               : -1;
-              }
-            }
-            if (lane == 0) {
-              S.t0[e] = pt0;
-              S.whole[e] = box && all == 0xffffffffu;
-              pt_release(&S.vmtag[v], 2u * (uint32_t)x + (all == 0xffffffffu ? 1u : 0u));
+              const int t = t0 + lane + 32 * k;
+              const bool page = ent[k] >= 0 && ent[k] < C.n_pages;
+              S.row[e][lane + 32 * k] = page ? (int64_t)ent[k] * C.page_stride +
+                                                   (int64_t)(t - div_by(P.page, t) * C.page_tokens) * C.row_stride
+                                             : -1;
             }
           }
-          __syncwarp();
           if (lane == 0) {
-            S.kvh[e] = pkvh;
-            mbar_arrive(&S.ufull[e]);
+            S.t0[e] = t0;
+            S.whole[e] = box && all == 0xffffffffu;
+            pt_release(&S.vmtag[v], 2u * (uint32_t)(x + 1) + (all == 0xffffffffu ? 1u : 0u));
           }
-          if (pkvh < 0) break;
         }
-        pkvh = more ? I.kvh : -1;
+        __syncwarp();
+        if (lane == 0) {
+          S.kvh[e] = more ? I.kvh : -1;
+          mbar_arrive(&S.ufull[e]);
+        }
+        if (!more) break;
       }
     } else if (warp == 10) {
       int nq[2] = {0, 0}, nitem = 0;
