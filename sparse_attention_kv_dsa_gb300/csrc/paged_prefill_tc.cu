@@ -16,7 +16,10 @@
 //   P_i = 2^(x - m) by four warps, one row a thread, bf16 back into TMEM over S_i
 //   O_i += P_i V   (A from TMEM, V as stored: MN-major)
 // in the order PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1): the tensor cores work on one tile while
-// the other's softmax runs.  The running maximum m of a row is only moved when a tile's
+// the other's softmax runs.  A row tile of 128 rows at most (a few drafted tokens over a long
+// cache) has no second tile to alternate with: its two halves of TMEM and of the softmax warps
+// then take its tiles of the cache in turn, each with its own O, m and l, joined at the end.
+// The running maximum m of a row is only moved when a tile's
 // maximum passes it by 2^8 (the weights stay below 256, exact in the float32 sums), so O is
 // rescaled in TMEM a few times in a long row and not with every tile.
 // TMEM columns: S_0 0-127, S_1 128-255 (P_i in the first 64 of S_i), O_0 256.., O_1 384...
@@ -51,8 +54,9 @@ struct PtShape {
 
 struct PtShared {
   uint64_t qfull[2], qempty[2], full[8], empty[8];
-  uint64_t sfull[2], pfull[2], pvdone[2], oempty[2];
+  uint64_t sfull[2], pfull[2], pvdone[2], oempty[2], mlfull;
   uint64_t ifull[PT_ITEMS], iempty[PT_ITEMS], ufull[PT_UNITS], uempty[PT_UNITS];
+  float2 ml[128];                    // (m, l) of the second half of a row tile whose tiles alternate
   uint32_t tmem_base;
   int fail;
   uint32_t vm[PT_VM][4];             // tokens there, of unit x in entry x % PT_VM
@@ -194,7 +198,7 @@ __device__ __forceinline__ uint32_t pt_bits(int a, int b) {
   return hi & ~lo;
 }
 
-template <int D, int MOD>
+template <int D, int MOD, bool ALT>
 __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const __grid_constant__ PrefillParams P,
                                                                         const __grid_constant__ CUtensorMap kmap,
                                                                         const __grid_constant__ CUtensorMap vmap,
@@ -223,6 +227,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     for (int i = 0; i < PT_ITEMS; ++i) { mbar_init(&S.ifull[i], 1); mbar_init(&S.iempty[i], 10); }
     for (int i = 0; i < PT_UNITS; ++i) { mbar_init(&S.ufull[i], 1); mbar_init(&S.uempty[i], 4); }
     for (int i = 0; i < PT_VM; ++i) S.vmtag[i] = 0;
+    mbar_init(&S.mlfull, 128);
     S.fail = 0;
     fence_mbar_init();
   }
@@ -433,8 +438,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       const uint64_t vd = smem_desc(ring, 128 * 128, 1024, LAYOUT_SW128);
       // slots and phases: keys of the unit whose scores come next, values of unit x
       uint32_t ks = 0, kph = 0, vs = 1, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, no[2] = {0, 0};
-      auto qk = [&](int t) {
-        const uint64_t ad = qd + (uint64_t)(t * (QB >> 4)), bd = kd + (uint64_t)(ks * (QB >> 4));
+      auto qk = [&](int t, int q) {                       // tile t's scores, of query tile q
+        const uint64_t ad = qd + (uint64_t)(q * (QB >> 4)), bd = kd + (uint64_t)(ks * (QB >> 4));
 #pragma unroll 1
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t o = (uint32_t)((k >> 2) * 1024 + (k & 3) * 2);
@@ -464,6 +469,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         ks += 2;
         if (ks >= SLOTS) { ks = 0; kph ^= 1; }
       };
+      auto next_values = [&]() {
+        vs += 2;
+        if (vs >= SLOTS) { vs = 1; vph ^= 1; }
+      };
       auto wait_queries = [&](int t) {
         ok = ok && pt_wait1(&S.qfull[t], qph[t]);
         qph[t] ^= 1;
@@ -488,14 +497,39 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           wait_keys();
           wait_queries(0);
           if (!ok) break;
-          qk(0);
+          qk(0, 0);
           if (two) {
             wait_queries(1);
             if (!ok) break;
-            qk(1);
+            qk(1, 1);
           }
           next_keys();
           first = true;
+          if (ALT && !two && left >= 2) {                        // its tiles in turn: unit j by half j & 1
+            wait_keys();
+            if (!ok) break;
+            qk(1, 0);
+            next_keys();
+            for (int j = 0; j < left && ok; ++j) {
+              const int t = j & 1;
+              const bool more = j + 2 < left;
+              if (more) wait_keys();
+              ok = ok && pt_wait1(&S.full[vs], vph);
+              fence_proxy_async_smem();
+              if (ok) pv(t, j < 2);
+              if (!ok) break;
+              if (more) {
+                qk(t, 0);
+                next_keys();
+              } else {
+                mma_commit(&S.pvdone[t]);
+              }
+              next_values();
+            }
+            if (!ok) break;
+            go = take();
+            continue;
+          }
         }
         fresh = left == 1;                                // unit x + 1 begins a row tile
         if (!fresh) wait_keys();
@@ -503,16 +537,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         fence_proxy_async_smem();
         pv(0, first);
         if (!ok) break;
-        if (!fresh) qk(0);
+        if (!fresh) qk(0, 0);
         if (fresh) mma_commit(&S.pvdone[0]);               // the epilogue's
         if (two) {
           pv(1, first);
           if (!ok) break;
-          if (!fresh) qk(1);
+          if (!fresh) qk(1, 1);
           if (fresh) mma_commit(&S.pvdone[1]);
         }
-        vs += 2;
-        if (vs >= SLOTS) { vs = 1; vph ^= 1; }
+        next_values();
         if (!fresh) {
           next_keys();
           --left;
@@ -529,9 +562,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     const int t = warp >> 2;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = trow + 128u * t, to = trow + 256u + 128u * t;
-    const int r = t * 128 + (warp & 3) * 32 + lane;       // row of the row tile
+    const int wr = (warp & 3) * 32 + lane;                // row of the tile
     const float aa = fmaxf(P.f.a, 1e-37f);                // a scale of 0 keeps masked scores at -inf
-    int x = 0, nitem = 0, ns = 0, nd = 0;                 // units, row tiles, this tile's units and row tiles so far
+    // units, row tiles, this half's units and its finished sums (with row tiles that alternate:
+    // both halves'), such row tiles, and value tiles of the last row tile not handed back, so far
+    int x = 0, nitem = 0, ns = 0, nd[2] = {0, 0}, nalt = 0, vrem = 0;
     while (ok) {
       const int e = nitem % PT_ITEMS;
       if (!pt_wait(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; break; }
@@ -539,19 +574,24 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       const RowTile &I = S.item[e];
       const int i0 = I.i0, i1 = I.i1;
       if (i1 < 0) break;
-      if (t == 1 && I.nr <= 128) {
+      const bool two = I.nr > 128, alt = ALT && !two && i1 - i0 >= 2;
+      if (t == 1 && !two && !alt) {
         x += i1 - i0;
+        if (ALT) {
+          ++nd[0];
+          vrem = 1;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.iempty[e]);
         continue;
       }
+      const int r = (alt ? 0 : t * 128) + wr;             // row of the row tile
       const int len = I.len, n = I.n, nr = I.nr, r0 = I.r0, s0 = I.s0, kvh = I.kvh, elsewhere = I.elsewhere, c0 = I.c0;
       const TileSpan span = I.span;
-      const int last_t = nr > 128 ? 1 : 0;                // the tile whose products are issued last
       int pre = I.pre;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.iempty[e]);
-      const bool there = r < nr, some = t * 128 + (warp & 3) * 32 < nr;
+      const bool there = r < nr, some = r - lane < nr;
       const int tk = there ? div_by(P.group, r0 + r) : 0, hd = there ? kvh * G + (r0 + r) - tk * G : 0;
       int pos = len - n + tk, first = 0, lo = 0;
       if (!there || pos < 0) {
@@ -570,15 +610,24 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       const int pa = __reduce_max_sync(0xffffffffu, there ? (int)(((unsigned)first + PT_KEYS - 1) / PT_KEYS) : 0);
       const int pb = __reduce_min_sync(0xffffffffu, there ? pre / PT_KEYS : 0x7fffffff);
       float m = -INFINITY, l = 0.f;
-      for (int i = i0; i < i1; ++i, ++x, ++ns) {
+      const int step = alt ? 2 : 1;
+      int i = i0;
+      if (alt) i += t, x += t;
+      for (; i < i1; i += step, x += step, ++ns) {
         if (!pt_wait(&S.sfull[t], ns & 1)) { ok = false; break; }
         tc_fence_after();
         if ((warp & 3) == 0 && lane == 0) {                // every product up to this QK is done
-          if (t == last_t) {
+          if (alt || t == (two ? 1 : 0)) {                 // (of two tiles' the second is issued last)
             mbar_arrive(&S.empty[(2 * x) % SLOTS]);
-            if (x > 0) mbar_arrive(&S.empty[(2 * x - 1) % SLOTS]);
+            if (!ALT) {
+              if (x > 0) mbar_arrive(&S.empty[(2 * x - 1) % SLOTS]);
+            } else if (i - step >= i0) {
+              mbar_arrive(&S.empty[(2 * (x - step) + 1) % SLOTS]);
+            } else if (i == i0) {
+              for (int k = 1; k <= vrem; ++k) mbar_arrive(&S.empty[(2 * (x - k) + 1) % SLOTS]);
+            }
           }
-          if (i + 1 == i1) mbar_arrive(&S.qempty[t]);
+          if (i + 1 == i1) mbar_arrive(&S.qempty[alt ? 0 : t]);
         }
         if (some) {
           const int ti = span.tile(i), t0 = ti * PT_KEYS;
@@ -660,7 +709,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           // move the maximum when it is passed by 2^8, or was none (PV of the tile before was
           // issued ahead of this tile's QK: it is done)
           const float nm = mx > m + 8.f ? mx : m;
-          if (i == i0) {
+          if (i < i0 + step) {
             m = mx;
           } else if (__any_sync(0xffffffffu, nm != m)) {
             const float corr = nm != m ? ex2(m - nm) : 1.f;
@@ -708,8 +757,36 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       }
       if (!ok) break;
       // ---- epilogue
-      if (!pt_wait(&S.pvdone[t], nd & 1)) { ok = false; break; }
-      ++nd;
+      if (alt) x -= i - i1;
+      vrem = step;
+      float f0 = 1.f, f1 = 0.f;
+      if (alt) {
+        // half 0 joins both: O_1 from its own lanes of TMEM, (m, l) through shared memory, which
+        // half 0 has read by the time it gives O_1 up
+        if (t == 1) {
+          if (nd[1] && !pt_wait(&S.oempty[1], (nd[1] - 1) & 1)) { ok = false; break; }
+          S.ml[wr] = make_float2(m, l);
+          mbar_arrive(&S.mlfull);
+        } else if (!pt_wait(&S.mlfull, nalt & 1) || !pt_wait(&S.pvdone[0], nd[0] & 1)) {
+          ok = false;
+          break;
+        }
+        if (!pt_wait(&S.pvdone[1], nd[1] & 1)) { ok = false; break; }
+        ++nalt;
+        ++nd[0];
+        ++nd[1];
+        if (t == 1) continue;
+        const float2 o = S.ml[wr];
+        const float nm = fmaxf(m, o.x), z = nm == -INFINITY ? 0.f : nm;
+        f0 = ex2(m - z);
+        f1 = ex2(o.x - z);
+        m = nm;
+        l = l * f0 + o.y * f1;
+      } else {
+        if (!pt_wait(&S.pvdone[t], nd[ALT ? t : 0] & 1)) { ok = false; break; }
+        ++nd[0];
+        if (ALT && two) ++nd[1];
+      }
       tc_fence_after();
       const bool done = elsewhere == 0;
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
@@ -720,6 +797,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         for (int k = 0; k < D; k += 32) {
           uint32_t o[32];
           tmem_ld32(to + k, o);
+          if (alt) {
+            uint32_t o1[32];
+            tmem_ld32(to + 128 + k, o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f0 + __uint_as_float(o1[q]) * f1);
+          }
           tmem_wait_ld();
           if (there) {
             if (done) {
@@ -750,6 +834,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       }
       tc_fence_before();
       mbar_arrive(&S.oempty[t]);
+      if (alt) mbar_arrive(&S.oempty[1]);
       if (there) {
         if (done) P.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPgLn2;
         else *reinterpret_cast<float2 *>(P.pml + prow * 2) = make_float2(m, l);
@@ -800,10 +885,10 @@ static bool bf16_map(CUtensorMap *m, const void *base, int nd, const int64_t *di
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int MOD>
+template <int D, int MOD, bool ALT>
 static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
   static_assert(pt_smem<D>() <= 227 * 1024, "fits an SM");
-  ECHO_CUDA_OK((allow_smem<paged_prefill_tc_kernel<D, MOD>>(pt_smem<D>())));
+  ECHO_CUDA_OK((allow_smem<paged_prefill_tc_kernel<D, MOD, ALT>>(pt_smem<D>())));
   int box = std::min(P.C.page_tokens & -P.C.page_tokens, PT_KEYS), qbox = 128 % P.G == 0 ? 128 / P.G : 0;
   CUtensorMap kmap = {}, vmap = {}, qmap = {};
   {
@@ -821,7 +906,7 @@ static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
     if (qbox && !bf16_map(&qmap, P.q, 3, qd, qs, qb)) qbox = 0;
   }
   const int grid = std::min(sm_count(), PF_MAX_CTAS / 2);
-  paged_prefill_tc_kernel<D, MOD><<<grid, PT_THREADS, pt_smem<D>(), st>>>(P, kmap, vmap, qmap, box, qbox);
+  paged_prefill_tc_kernel<D, MOD, ALT><<<grid, PT_THREADS, pt_smem<D>(), st>>>(P, kmap, vmap, qmap, box, qbox);
   ECHO_LAUNCH_OK();
   ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<__nv_bfloat16, D>, dim3(grid, (P.prows + 3) / 4), dim3(128), st, P));
   return ECHO_OK;
@@ -831,10 +916,21 @@ template <int D>
 static echo_status_t launch_mod(PrefillParams &P, cudaStream_t st) {
   // a negative scale goes with the bias: the plain form takes the largest raw product
   const int mod = (P.f.capped ? 1 : 0) | (P.slopes || P.f.a < 0.f ? 2 : 0);
-  return mod == 0 ? launch_tc<D, 0>(P, st)
-       : mod == 1 ? launch_tc<D, 1>(P, st)
-       : mod == 2 ? launch_tc<D, 2>(P, st)
-                  : launch_tc<D, 3>(P, st);
+  // Row tiles of one query tile alternate over the cache only in a kernel of their own: four
+  // drafted tokens each of 16 sequences of 20K go from 227 to 207 us with it, a prompt of 8192
+  // from 1000 to 1080 (its loop then spills).  Taken where a sequence's rows on average fit one
+  // query tile; either kernel is right for any mixture.
+  const bool alt = (int64_t)P.N * P.G <= 128 * (int64_t)P.B;
+  switch (2 * mod + (alt ? 1 : 0)) {
+    case 0: return launch_tc<D, 0, false>(P, st);
+    case 1: return launch_tc<D, 0, true>(P, st);
+    case 2: return launch_tc<D, 1, false>(P, st);
+    case 3: return launch_tc<D, 1, true>(P, st);
+    case 4: return launch_tc<D, 2, false>(P, st);
+    case 5: return launch_tc<D, 2, true>(P, st);
+    case 6: return launch_tc<D, 3, false>(P, st);
+    default: return launch_tc<D, 3, true>(P, st);
+  }
 }
 
 echo_status_t launch_prefill_tc(PrefillParams &P, cudaStream_t st) {

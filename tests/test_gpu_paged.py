@@ -332,6 +332,24 @@ def test_scales_of_zero_and_below(scale):
         check_rows("token", out, lse, tuple(x[-1:] for x in ref))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", [dict(), dict(window=200), dict(cap=5.0, q_scale=6.0, alibi=True), dict(docs=200),
+                                dict(prefix=True, alibi=True), dict(empty=True)])
+def test_prefill_short_runs_of_rows_beside_long_ones(d, kw):
+    # a few new tokens each over caches of one tile, two and many, between prompts of several row
+    # tiles: row tiles of one query tile and of two follow one another on a CTA
+    kw = dict(kw)
+    new = [(1, 4, 3, 150, 4, 0, 2, 33, 4, 4, 60)[i % 11] for i in range(37)]
+    lens = [n + (0, 700, 120, 9, 128, 5, 1000, 256, 129, 2000, 380)[(i * 5) % 11] for i, n in enumerate(new)]
+    if kw.pop("prefix", None):
+        kw["prefix"] = [(0, 300, 5)[i % 3] for i in range(37)]
+    if kw.pop("empty", None):
+        # half of every sequence's rows see nothing, one in three only their last tokens
+        kw["first"] = [p + 1 if p % 2 else (max(0, p - 40) if p % 3 == 0 else 0)
+                       for n, m in zip(lens, new) for p in range(n - m, n)]
+    _prefill(lens, new, 16, 8, 2, d, BF, seed=51, tail_rows=2, **kw)
+
+
 def test_prefill_many_sequences():
     new = [i % 4 for i in range(300)]
     _prefill([n + (11 * i) % 40 for i, n in enumerate(new)], new, 8, 4, 2, 64, BF, seed=35)
