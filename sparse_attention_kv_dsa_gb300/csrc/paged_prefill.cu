@@ -10,7 +10,11 @@
 // Float32 (below), two CTAs an SM: row tiles of 64 packed rows, 64-token tiles of the cache, a
 // running maximum and sum; 256 threads hold 4 x 4 scores and 4 x d/16 results each.  Float32
 // arithmetic throughout: 4 d operations for each pair of query head and seen token on the FMA
-// units, which bound it.
+// units, which bound it together with shared memory (eight 16-byte loads to 64 FMAs).
+//
+// Measured on a GB300: two sequences of 600-1100 tokens, 8 heads of 64 over 4, two-way prefix,
+// 59 us (1.2 GFLOP; FMA issue 42 %, shared memory 52 %, one wave of 304 CTAs); 129 us with a CTA a row
+// tile, which leaves the last rows of a causal mask to few of them.
 
 #include "paged_prefill.cuh"
 

@@ -76,6 +76,16 @@ def test_null_and_sizes():
         assert append(cache(), rot=rot) == UNS
 
 
+def test_work_that_32_bits_cannot_count():
+    # 2^31 - 2^16 tokens of a sequence are the most that a table may hold; then 33.5M 64-token tiles
+    big = dict(max_pages=32767, page_tokens=65536)
+    assert decode(cache(max_pages=32768, page_tokens=65536), scores()) == UNS
+    assert decode(cache(**big), scores(), B=1000) == UNS
+    assert prefill(cache(**big), scores(), N=70000) == UNS
+    assert prefill(cache(), scores(), N=2049, B=2049) == UNS
+    assert prefill(cache(), scores(), N=0x7fffffff, nbytes=1 << 40) == UNS
+
+
 def test_struct_layouts_and_workspaces():
     out = (ctypes.c_size_t * 2)()
     E.lib().echo_paged_struct_sizes(out)
