@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     S.fail = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 11) {
     tmem_alloc(&S.tmem_base, 512);
     tmem_relinquish();
   }
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         if (nq[h]) pt_wait(&S.qfull[h], (nq[h] - 1) & 1);
     }
     if (warp == 10) cp_async_wait_all();
-    if (warp == 8 && pt_elect()) {
+    if (warp == 11 && pt_elect()) {
     // ------------------------------------------------------------------ MMA --
       // One thread issues everything, and the tensor cores wait whenever it is late: what can be
       // waited for early (the keys of unit x + 1 and the values of x) is, before the weights of
@@ -444,122 +444,74 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       const uint64_t qd = smem_desc(smem_u32(R), 16, 1024, LAYOUT_SW128);
       const uint64_t kd = smem_desc(ring, 16, 1024, LAYOUT_SW128);
       const uint64_t vd = smem_desc(ring, 128 * 128, 1024, LAYOUT_SW128);
-      // slots and phases: keys of the unit whose scores come next, values of unit x
-      uint32_t ks = 0, kph = 0, vs = 1, vph = 0, qph[2] = {0, 0}, pph[2] = {0, 0}, no[2] = {0, 0};
-      auto qk = [&](int t, int q) {                       // tile t's scores, of query tile q
-        const uint64_t ad = qd + (uint64_t)(q * (QB >> 4)), bd = kd + (uint64_t)(ks * (QB >> 4));
-#pragma unroll 1
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = (uint32_t)((k >> 2) * 1024 + (k & 3) * 2);
-          mma_f16(tmem + 128u * t, ad + o, bd + o, id_qk, k ? 1u : 0u);
-        }
-        mma_commit(&S.sfull[t]);
-      };
-      auto pv = [&](int t, bool first) {
-        if (!pt_wait1(&S.pfull[t], pph[t])) { ok = false; return; }
-        pph[t] ^= 1;
-        if (first) {
-          if (no[t] && !pt_wait1(&S.oempty[t], (no[t] - 1) & 1)) { ok = false; return; }
-          ++no[t];
-        }
-        tc_fence_after();
-        const uint64_t bd = vd + (uint64_t)(vs * (QB >> 4));
-#pragma unroll 1
-        for (int k = 0; k < PT_KEYS / 16; ++k)
-          pt_mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * k, bd + 128 * k, id_pv, (!first || k) ? 1u : 0u);
-      };
-      auto wait_keys = [&]() {
-        ok = ok && pt_wait1(&S.full[ks], kph);
-        fence_proxy_async_smem();                         // the loaders' cp.async writes, for the tensor cores
-        tc_fence_after();
-      };
-      auto next_keys = [&]() {
-        ks += 2;
-        if (ks >= SLOTS) { ks = 0; kph ^= 1; }
-      };
-      auto next_values = [&]() {
-        vs += 2;
-        if (vs >= SLOTS) { vs = 1; vph ^= 1; }
-      };
-      auto wait_queries = [&](int t) {
-        ok = ok && pt_wait1(&S.qfull[t], qph[t]);
-        qph[t] ^= 1;
-        fence_proxy_async_smem();
-        tc_fence_after();
-      };
-      int nitem = 0, left = 0;                            // units of the row tile from unit x on
-      bool two = false;
-      auto take = [&]() {                                 // the next row tile; false: no more
-        const int e = nitem % PT_ITEMS;
-        if (!pt_wait1(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; return false; }
-        const int i1 = S.item[e].i1;
-        left = i1 - S.item[e].i0;
-        two = S.item[e].nr > 128;
+      // slots and phases: keys of the unit whose scores come next, values of unit x; phase bits
+      // of the tiles' queries and weights, and of the O that an epilogue gives back
+      uint32_t ks = 0, kph = 0, vs = 1, vph = 0, qph = 0, pph = 0, oph = 3;
+      int nitem = 0;
+      while (ok) {
+        const int e = nitem % PT_ITEMS;                   // the next row tile
+        if (!pt_wait1(&S.ifull[e], (nitem / PT_ITEMS) & 1)) { ok = false; break; }
+        const int i1 = S.item[e].i1, n = i1 - S.item[e].i0;
+        const bool two = S.item[e].nr > 128;
         mbar_arrive(&S.iempty[e]);
         ++nitem;
-        return i1 >= 0;
-      };
-      bool go = take(), first = true, fresh = true;       // first: unit x is its row tile's first
-      while (go) {
-        if (fresh) {                                      // the first scores of a row tile
-          wait_keys();
-          wait_queries(0);
-          if (!ok) break;
-          qk(0, 0);
-          if (two) {
-            wait_queries(1);
-            if (!ok) break;
-            qk(1, 1);
-          }
-          next_keys();
-          first = true;
-          if (ALT && !two && left >= 2) {                        // its tiles in turn: unit j by half j & 1
-            wait_keys();
-            if (!ok) break;
-            qk(1, 0);
-            next_keys();
-            for (int j = 0; j < left && ok; ++j) {
-              const int t = j & 1;
-              const bool more = j + 2 < left;
-              if (more) wait_keys();
-              ok = ok && pt_wait1(&S.full[vs], vph);
-              fence_proxy_async_smem();
-              if (ok) pv(t, j < 2);
-              if (!ok) break;
-              if (more) {
-                qk(t, 0);
-                next_keys();
-              } else {
-                mma_commit(&S.pvdone[t]);
+        if (i1 < 0) break;
+        // Step j: the values of unit j, then the scores of unit j + lag into the S that they left;
+        // of both tiles, or of the half whose turn it is.  One rolled body for the first scores,
+        // the loop and the last values: what this thread runs has to stay in the instruction
+        // cache beside the softmax.
+        const int lag = ALT && !two && n >= 2 ? 2 : 1;
+#pragma unroll 1
+        for (int j = -lag; ok && j < n; ++j) {
+          const bool more = j + lag < n;
+          if (more) ok = pt_wait1(&S.full[ks], kph);
+          if (j >= 0) ok = ok && pt_wait1(&S.full[vs], vph);
+          fence_proxy_async_smem();                       // the loaders' cp.async writes, for the tensor cores
+#pragma unroll 1
+          for (int h = 0; ok && h <= (two ? 1 : 0); ++h) {
+            const int t = lag == 2 ? j & 1 : h;
+            const uint32_t bit = 1u << t, st = tmem + 128u * t;
+            if (j >= 0) {
+              ok = pt_wait1(&S.pfull[t], (pph >> t) & 1u);
+              pph ^= bit;
+              if (j < lag) {                              // the row tile's first values
+                ok = ok && pt_wait1(&S.oempty[t], (oph >> t) & 1u);
+                oph ^= bit;
               }
-              next_values();
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t bd = vd + (uint64_t)(vs * (QB >> 4));
+#pragma unroll 4
+              for (int k = 0; k < PT_KEYS / 16; ++k)
+                pt_mma_ts(st + 256u, st + 8u * k, bd + 128 * k, id_pv, (j >= lag || k) ? 1u : 0u);
             }
-            if (!ok) break;
-            go = take();
-            continue;
+            if (more) {
+              if (j < 0 && (lag == 1 || j == -2)) {
+                ok = pt_wait1(&S.qfull[h], (qph >> h) & 1u);
+                qph ^= 1u << h;
+                if (!ok) break;
+                fence_proxy_async_smem();
+              }
+              tc_fence_after();
+              const uint64_t ad = qd + (uint64_t)(h * (QB >> 4)), bd = kd + (uint64_t)(ks * (QB >> 4));
+#pragma unroll 4
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t o = (uint32_t)((k >> 2) * 1024 + (k & 3) * 2);
+                mma_f16(st, ad + o, bd + o, id_qk, k ? 1u : 0u);
+              }
+              mma_commit(&S.sfull[t]);
+            } else {
+              mma_commit(&S.pvdone[t]);                   // the epilogue's
+            }
           }
-        }
-        fresh = left == 1;                                // unit x + 1 begins a row tile
-        if (!fresh) wait_keys();
-        if (!ok || !pt_wait1(&S.full[vs], vph)) { ok = false; break; }
-        fence_proxy_async_smem();
-        pv(0, first);
-        if (!ok) break;
-        if (!fresh) qk(0, 0);
-        if (fresh) mma_commit(&S.pvdone[0]);               // the epilogue's
-        if (two) {
-          pv(1, first);
-          if (!ok) break;
-          if (!fresh) qk(1, 1);
-          if (fresh) mma_commit(&S.pvdone[1]);
-        }
-        next_values();
-        if (!fresh) {
-          next_keys();
-          --left;
-          first = false;
-        } else {
-          go = take();
+          if (more) {
+            ks += 2;
+            if (ks >= SLOTS) { ks = 0; kph ^= 1; }
+          }
+          if (j >= 0) {
+            vs += 2;
+            if (vs >= SLOTS) { vs = 1; vph ^= 1; }
+          }
         }
       }
     }
@@ -856,7 +808,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 11) tmem_dealloc(tmem, 512);
   if (S.fail && tid == 0) {
     P.rec[blockIdx.x * 8] = 0;
     paged_fail(C.status, ECHO_ERR_TIMEOUT);
