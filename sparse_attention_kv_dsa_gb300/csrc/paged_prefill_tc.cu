@@ -24,7 +24,7 @@
 // rescaled in TMEM a few times in a long row and not with every tile.
 // TMEM columns: S_0 0-127, S_1 128-255 (P_i in the first 64 of S_i), O_0 256.., O_1 384...
 // Warps 0-3 and 4-7: softmax and epilogue of tile 0 and 1 (192 registers: a row's 128 scores
-// stay in registers); warp 8: MMA issue; warp 9: the walk over the units and their page-table
+// stay in registers); warp 11: MMA issue; warp 9: the walk over the units and their page-table
 // look-ups; warp 10: the queries; warps 12, 13: the keys; 14, 15: the values.  A tile of the
 // cache whose 128 tokens are all seen by some row comes by TMA, in boxes of the largest power of two of rows
 // that divides a page (8 or more, the period of the swizzle); the tiles at the ends of the
@@ -33,12 +33,15 @@
 // share a tile: 16-row pages need 16 boxes of it.
 //
 // Measured on a GB300 (cuBLAS bf16 1.94 PFLOP/s): a prompt of 8192, 64 heads of 128 over 8,
-// 1.00 ms, 1.1 PFLOP/s, bound by the round from one product over the softmax to the next and by
-// the power cap (the clock falls to 1.5 GHz); 512 tokens over 32K, capped, 347 us, 0.79 PFLOP/s
-// (the polynomial tanh's issue slots); 16 x 4 drafted tokens over 17K-20K, 207 us, 5.9 TB/s;
-// 8 packed prompts with documents and distance bias, 51 us, of which the plan, the first run of
-// the code and the joins are some 20.  Not kept: P handed over in two halves (1267 us for the
-// prompt), 32-column stores of P.
+// 0.93 ms, 1.18 PFLOP/s, bound by each tile's own round: 1500 cycles of softmax, 250 until the
+// products start, 1370 for both of them; 512 tokens over 32K, capped, 330 us, 0.83 PFLOP/s (a
+// softmax of 4000 cycles, with the polynomial tanh); 16 x 4 drafted tokens over 17K-20K, 207 us, 5.9 TB/s;
+// 8 packed prompts with documents and distance bias, 50 us, of which the plan, the first run of
+// the code and the joins are some 20.  Instruction fetch is part of every one of these figures:
+// the issuing thread with its products unrolled for both tiles took 1000 and 347 us.  Not kept: P
+// handed over in two halves (1267 us for the prompt), 32-column stores of P, scores read from
+// TMEM twice in 32-column steps (1060 us rolled, 1131 unrolled; capped chunk 374 and 387), the
+// second half of the scores loaded under the first one's maximum (953 us, capped chunk 350).
 
 #include <atomic>
 #include <cudaTypedefs.h>
@@ -877,7 +880,7 @@ static echo_status_t launch_mod(PrefillParams &P, cudaStream_t st) {
   // a negative scale goes with the bias: the plain form takes the largest raw product
   const int mod = (P.f.capped ? 1 : 0) | (P.slopes || P.f.a < 0.f ? 2 : 0);
   // Row tiles of one query tile alternate over the cache only in a kernel of their own: four
-  // drafted tokens each of 16 sequences of 20K go from 227 to 207 us with it, a prompt of 8192
+  // drafted tokens each of 16 sequences of 20K went from 227 to 207 us with it, a prompt of 8192
   // from 1000 to 1080 (its loop then spills).  Taken where a sequence's rows on average fit one
   // query tile; either kernel is right for any mixture.
   const bool alt = (int64_t)P.N * P.G <= 128 * (int64_t)P.B;
