@@ -33,13 +33,13 @@
 // share a tile: 16-row pages need 16 boxes of it.
 //
 // Measured on a GB300 (cuBLAS bf16 1.94 PFLOP/s): a prompt of 8192, 64 heads of 128 over 8,
-// 0.93 ms, 1.18 PFLOP/s, bound by each tile's own round: 1500 cycles of softmax, 250 until the
-// products start, 1370 for both of them; 512 tokens over 32K, capped, 330 us, 0.83 PFLOP/s (a
+// 0.91 ms, 1.2 PFLOP/s, bound by each tile's own round: 1500 cycles of softmax, 250 until the
+// last products start, 1000 to 1300 for them; 512 tokens over 32K, capped, 327 us, 0.83 PFLOP/s (a
 // softmax of 4000 cycles, with the polynomial tanh); 16 x 4 drafted tokens over 17K-20K, 207 us, 5.9 TB/s;
 // 8 packed prompts with documents and distance bias, 50 us, of which the plan, the first run of
 // the code and the joins are some 20.  Instruction fetch is part of every one of these figures:
-// the issuing thread with its products unrolled for both tiles took 1000 and 347 us.  Not kept: P
-// handed over in two halves (1267 us for the prompt), 32-column stores of P, scores read from
+// the issuing thread with its products unrolled for both tiles took 1000 and 347 us.  Handing P
+// over in two parts gains 25 us of the prompt and 3 of the capped chunk.  Not kept: 32-column stores of P, scores read from
 // TMEM twice in 32-column steps (1060 us rolled, 1131 unrolled; capped chunk 374 and 387), the
 // second half of the scores loaded under the first one's maximum (953 us, capped chunk 350).
 
@@ -65,7 +65,7 @@ struct PtShape {
 
 struct PtShared {
   uint64_t qfull[2], qempty[2], full[8], empty[8];
-  uint64_t sfull[2], pfull[2], pvdone[2], oempty[2], mlfull;
+  uint64_t sfull[2], pfull[2], pmost[2], pvdone[2], oempty[2], mlfull;
   uint64_t ifull[PT_ITEMS], iempty[PT_ITEMS], ufull[PT_UNITS], uempty[PT_UNITS];
   float2 ml[128];                    // (m, l) of the second half of a row tile whose tiles alternate
   uint32_t tmem_base;
@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       mbar_init(&S.qempty[i], 1);
       mbar_init(&S.sfull[i], 1);
       mbar_init(&S.pfull[i], 128);
+      mbar_init(&S.pmost[i], 128);
       mbar_init(&S.pvdone[i], 1);
       mbar_init(&S.oempty[i], 128);
     }
@@ -475,8 +476,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
             const int t = lag == 2 ? j & 1 : h;
             const uint32_t bit = 1u << t, st = tmem + 128u * t;
             if (j >= 0) {
-              ok = pt_wait1(&S.pfull[t], (pph >> t) & 1u);
-              pph ^= bit;
+              ok = pt_wait1(&S.pmost[t], (pph >> t) & 1u); // weights of the first 96 tokens
               if (j < lag) {                              // the row tile's first values
                 ok = ok && pt_wait1(&S.oempty[t], (oph >> t) & 1u);
                 oph ^= bit;
@@ -485,8 +485,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
               tc_fence_after();
               const uint64_t bd = vd + (uint64_t)(vs * (QB >> 4));
 #pragma unroll 4
-              for (int k = 0; k < PT_KEYS / 16; ++k)
+              for (int k = 0; k < 3 * PT_KEYS / 64; ++k)
                 pt_mma_ts(st + 256u, st + 8u * k, bd + 128 * k, id_pv, (j >= lag || k) ? 1u : 0u);
+              ok = pt_wait1(&S.pfull[t], (pph >> t) & 1u);
+              pph ^= bit;
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 3 * PT_KEYS / 64; k < PT_KEYS / 16; ++k)
+                pt_mma_ts(st + 256u, st + 8u * k, bd + 128 * k, id_pv, 1u);
             }
             if (more) {
               if (j < 0 && (lag == 1 || j == -2)) {
@@ -706,6 +713,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
               const __nv_bfloat162 h = __floats2bfloat162_rn(a, c);
               pk[q >> 1] = *reinterpret_cast<const uint32_t *>(&h);
             }
+            if (k == 3) {
+              pt_wait_st();
+              tc_fence_before();
+              mbar_arrive(&S.pmost[t]);                    // three quarters: their product can start
+            }
             pt_st16(ts + 16 * k, pk);
           }
           {
@@ -714,6 +726,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
             l += a + c;
           }
           pt_wait_st();
+        } else {
+          mbar_arrive(&S.pmost[t]);
         }
         tc_fence_before();
         mbar_arrive(&S.pfull[t]);
