@@ -620,7 +620,9 @@ echo_status_t echo_expand_block_slots(const int32_t *sel_blk, const int32_t *blo
  *   - q_start [B+1] (device, q_start[0] = 0, not descending): sequence b's new tokens are
  *     rows q_start[b] .. q_start[b+1]-1 of the packed arrays; row i of n_b sits at position
  *     seq_len[b] - n_b + i.  Rows from q_start[B] on are left as they were.  Entries are
- *     cut to [0, N]; sequences that would overlap are the caller's error.
+ *     cut to [0, N].  A q_start that descends is the caller's error: echo_paged_attn_prefill
+ *     then sets INVALID_ARG and writes nothing, echo_paged_append writes rows of some of the
+ *     positions that it names.
  *   - Only page-table entries of tokens that a call writes, or that some row of it sees,
  *     are used.  One outside [0, n_pages) sets ECHO_ERR_PAGE and its tokens are skipped.
  *     Rows of the pages that hold no token of the sequence (at or past seq_len) may hold

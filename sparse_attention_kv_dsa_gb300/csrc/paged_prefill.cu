@@ -13,7 +13,7 @@
 // units, which bound it together with shared memory (eight 16-byte loads to 64 FMAs).
 //
 // Measured on a GB300: two sequences of 600-1100 tokens, 8 heads of 64 over 4, two-way prefix,
-// 57 us (1.2 GFLOP; loops unrolled half as far 59; FMA issue 42 %, shared memory 52 %, one wave of 304 CTAs); 129 us with a CTA a row
+// 59 us (1.2 GFLOP; FMA issue 42 %, shared memory 52 %, one wave of 304 CTAs); 129 us with a CTA a row
 // tile, which leaves the last rows of a causal mask to few of them.
 
 #include "paged_prefill.cuh"

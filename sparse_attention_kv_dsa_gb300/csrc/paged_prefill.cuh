@@ -147,17 +147,20 @@ __device__ __forceinline__ RunPlan prefill_plan(const PrefillParams &P, PlanShar
   RunPlan pl;
   if (tid == 0) S.found = -1;
   uint32_t base = 0, sum;
+  bool bad = false;                                       // q_start descends
 #pragma unroll 1
   for (int b0 = 0; b0 < P.B; b0 += THREADS) {
     const int b = b0 + tid;
     const uint32_t n = b < P.B ? (uint32_t)(((int64_t)seq_rows(P, b).n * P.G + ROWS - 1) / ROWS) : 0;
+    bad |= b < P.B && min(P.q_start[b], P.N) > max(P.q_start[b + 1], 0);
     const uint32_t end = base + plan_scan<THREADS>(S, n, sum);
     if (b < P.B) S.tiles[b] = (int)(end - n);
     base += sum;
   }
   if (tid == 0) S.tiles[P.B] = (int)base;
-  pl.ntiles = (int)base;
-  __syncthreads();
+  // sequences that overlap: nothing bounds their row tiles' number, no work is done
+  if (bad) paged_fail(P.C.status, ECHO_ERR_INVALID_ARG);
+  pl.ntiles = __syncthreads_or(bad) ? 0 : (int)base;
   // PLAN_TILES row tiles at a time: their weights, then a scan in which a thread takes a run of
   // them.  The first pass gives the total, the second (the same values, where they all fit) the
   // row tile that holds the CTA's first weight.  First tokens are read by up to eight lanes a

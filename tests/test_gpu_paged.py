@@ -381,6 +381,47 @@ def test_prefill_bad_pages_and_lengths():
     check_rows("the rest", out[50:], lse[50:], ref)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("qs,code", [([0, 0, 0, 0], E.OK), ([5, 5, 5, 5], E.OK), ([0, 60, 20, 80], E.ERR_INVALID_ARG),
+                                     ([0, 70, -5, 70], E.ERR_INVALID_ARG), ([100, 100, 90, 100], E.OK)])
+def test_prefill_without_rows_or_with_descending_starts(dtype, qs, code):
+    # (entries past the 80 rows are cut to 80: the last one has no row)
+    P = Paged([200, 100, 90], 16, 2, 64, dtype, seed=3)
+    q = torch.randn(80, 4, 64, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    out, lse = torch.full_like(q, 7.0), torch.full((80, 4), 7.0, device=DEV)
+    E.paged_attn_prefill(q, torch.tensor(qs, dtype=torch.int32, device=DEV), P.k, P.v, P.table, P.seq_len, 0.1,
+                         out=out, lse=lse, status=P.status)
+    torch.cuda.synchronize()
+    assert P.status.item() == code
+    assert bool(torch.all(out == 7.0)) and bool(torch.all(lse == 7.0))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_results_at_any_16_byte_boundary_and_a_dirty_workspace(dtype, d):
+    P = Paged([1500, 40, 700], 16, 2, d, dtype, seed=5)
+    g = torch.Generator().manual_seed(1)
+    c, off = 16 // dtype.itemsize, 8 // dtype.itemsize * 2
+
+    def shifted(*shape):                                 # 16 bytes past a 256-byte boundary
+        n = torch.Size(shape).numel()
+        return torch.empty(n + c, dtype=dtype, device=DEV)[off:off + n].view(shape)
+
+    q = shifted(150, 8, d).copy_(torch.randn(150, 8, d, generator=g))
+    qs = starts([100, 5, 45])
+    want = E.paged_attn_prefill(q, qs, P.k, P.v, P.table, P.seq_len, 0.1)
+    last = [99, 104, 149]
+    one = E.paged_attn_decode(q[last].contiguous(), P.k, P.v, P.table, P.seq_len, 0.1)
+    for n, call, ref in ((E.paged_prefill_workspace_bytes(150, 3, 8, 2, d), E.paged_attn_prefill, want),
+                         (E.paged_decode_workspace_bytes(8, 2, d), E.paged_attn_decode, one)):
+        ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+        out = shifted(*ref[0].shape)
+        x = (q, qs) if call is E.paged_attn_prefill else (q[last].contiguous(),)
+        got = call(*x, P.k, P.v, P.table, P.seq_len, 0.1, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        assert got[0] is out and torch.equal(out, ref[0]) and torch.equal(got[1], ref[1])
+
+
 # ---------------------------------------------------------------------- together --
 def test_a_request_from_prompt_to_tokens_in_one_graph():
     """Two requests: prompts appended and attended, then tokens one by one, the token step
