@@ -504,6 +504,43 @@ def test_results_do_not_change_between_calls(dtype):
         assert all(torch.equal(x, y) for x, y in zip(first, (*a, *b)))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_captured_prompt_call_serves_other_lengths(dtype):
+    # captured once over 64 rows, replayed with other rows, lengths and documents
+    P = Paged([900, 300, 40], 16, 2, 64, dtype, seed=8)
+    q = torch.randn(64, 8, 64, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    qs, first = starts([40, 20, 4]), torch.zeros(64, dtype=torch.int32, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(64, 8, device=DEV)
+    ws = torch.empty(E.paged_prefill_workspace_bytes(64, 3, 8, 2, 64), dtype=torch.uint8, device=DEV)
+
+    def call():
+        E.paged_attn_prefill(q, qs, P.k, P.v, P.table, P.seq_len, 0.1, first_tok=first, out=out, lse=lse, workspace=ws,
+                             status=P.status)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lens, new, f in (([900, 300, 40], [40, 20, 4], 0), ([700, 17, 0], [4, 4, 0], 0), ([64, 1, 1], [62, 1, 1], 10)):
+        qs.copy_(starts(new))
+        P.seq_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        first.fill_(f)
+        out.fill_(7.0)
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        r = 0
+        for b, (n, m) in enumerate(zip(lens, new)):
+            if m:
+                ref = attend(q[r:r + m].double().cpu(), P.K[b][:n], P.V[b][:n], range(n - m, n), 0.1, dtype=dtype,
+                             first=[f] * m)
+                check_rows(f"{m} of {n}", out[r:r + m], lse[r:r + m], ref)
+            r += m
+        assert bool(torch.all(out[r:] == 7.0))
+    assert P.status.item() == E.OK
+
+
 def test_given_stream_and_two_streams_at_once():
     P = Paged([3000, 64], 16, 2, 128, BF, seed=6)
     q = torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
