@@ -439,14 +439,16 @@ __global__ void __launch_bounds__(PD_THREADS, PdShape<T, D>::CTAS) paged_decode_
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this CTA's run: a scan over the sequences, PD_THREADS at a time; with few sequences one
-  // scan gives the total and finds the place
+  // scan gives the total and finds the place.  Whether it is found is known from the barrier behind
+  // the writes of S.seq and S.before, the same in every thread: nobody reads either ahead of it
   uint32_t total = 0, end = 0, n = 0, per = 0, u0 = 0, u1 = 0;
-  if (tid == 0) { S.seq = -1; P.rec[blockIdx.x * 4] = 0; }
+  bool found = false;
+  if (tid == 0) P.rec[blockIdx.x * 4] = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     uint32_t at = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < P.B && (pass == 0 || S.seq < 0); b0 += PD_THREADS) {
+    for (int b0 = 0; b0 < P.B && !found; b0 += PD_THREADS) {
       if (pass == 0 || P.B > PD_THREADS) {
         n = b0 + tid < P.B ? (uint32_t)(decode_span(P, b0 + tid, TILE).n() + 1) * (uint32_t)HH : 0;
         uint32_t x = n;
@@ -466,8 +468,9 @@ __global__ void __launch_bounds__(PD_THREADS, PdShape<T, D>::CTAS) paged_decode_
         }
       }
       if (pass == 1) {
-        if (end - n <= u0 && u0 < end) { S.seq = b0 + tid; S.before = end - n; }
-        __syncthreads();
+        const bool mine = end - n <= u0 && u0 < end;
+        if (mine) { S.seq = b0 + tid; S.before = end - n; }
+        found = __syncthreads_or(mine);
       }
     }
     if (pass == 0) {
@@ -478,6 +481,7 @@ __global__ void __launch_bounds__(PD_THREADS, PdShape<T, D>::CTAS) paged_decode_
       if (u0 >= total) return;
     }
   }
+  if (!found) return;                                    // (lengths that another stream changes between the passes)
 
   // ---- cursor of the look-ups (the same in every thread): tile ci of its part [i0, ce) of the
   // current (sequence, head group), which begins at weight ws
