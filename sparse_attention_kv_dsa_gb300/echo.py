@@ -512,22 +512,32 @@ def _like(t, q, dt, shape, where: str, name: str):
     return t
 
 
+def _empty(shape, dt, dev, stream, kept: bool = True):
+    """New memory that the call's kernels write.  On a stream of its own it is allocated there: a
+    block that the current stream freed may still have work of that stream before it, and the
+    given stream does not wait for that.  Recorded on the current stream, where a kept one is
+    likely used."""
+    if stream is None:
+        return torch.empty(shape, dtype=dt, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dt, device=dev)
+    if kept:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def _attn_buffers(q, out, lse, workspace, nbytes: int, stream, where: str):
     """out, lse and the workspace: the caller's, or new ones."""
     shape, dev = q.shape, q.device
-    o = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else _like(out, q, q.dtype, shape, where, "out")
-    l = torch.empty(shape[:2], dtype=_FL, device=dev) if lse is None else _like(lse, q, _FL, shape[:2], where, "lse")
+    o = _empty(shape, q.dtype, dev, stream) if out is None else _like(out, q, q.dtype, shape, where, "out")
+    l = _empty(shape[:2], _FL, dev, stream) if lse is None else _like(lse, q, _FL, shape[:2], where, "lse")
     if workspace is None:
-        w = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        w = _empty(nbytes, torch.uint8, dev, stream, kept=False)
     else:
         w = workspace
         if w.device != dev or not w.is_contiguous():
             _bad(where, "workspace: contiguous, on q's device")
         nbytes = w.nbytes
-    if stream is not None:
-        for t, given in ((o, out), (l, lse), (w, workspace)):
-            if given is None:
-                t.record_stream(stream)
     return o, l, w, nbytes
 
 
@@ -554,9 +564,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_len, *, q=None, q_out=N
     if q is not None:
         Hq, qs = _head_rows(q, N, d, dt, dev, w, "q")
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-            if stream is not None:
-                q_out.record_stream(stream)
+            q_out = _empty(q.shape, dt, q.device, stream)
         else:
             _like(q_out, q, dt, q.shape, w, "q_out")
         qp, op = q.data_ptr(), q_out.data_ptr()

@@ -45,3 +45,48 @@ def test_decode_small_calls_give_the_same_bits_every_time(dtype, d, B):
         call()
         bad += (out != want).sum() + (lse != wlse).sum()
     assert bad.item() == 0 and P.status.item() == E.OK
+
+
+# -------------------------------------------------------- a stream of the call's own --
+def _call_beside_pending_work(call, shapes):
+    """call() with default buffers on a stream of its own while the current stream still has work on blocks
+    of `shapes` (shape, type) that are already free again: writes to some of them and a read of
+    others.  Neither may meet the call's buffers."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [(torch.empty(s, dtype=t, device=DEV), torch.ones(s, dtype=t, device=DEV)) for s, t in shapes]
+    copies = [torch.empty(s, dtype=t, device=DEV) for s, t in shapes]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                       # some 50 ms
+    for (x, y), c in zip(held, copies):
+        x.fill_(3)
+        c.copy_(y)
+    del held, x, y
+    got = call()
+    torch.cuda.synchronize()
+    assert all(bool((c == 1).all()) for c in copies), "a pending read of a freed block"
+    return got
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_default_buffers_on_a_given_stream_with_work_pending_on_the_current_one(dtype):
+    Hq, Hkv, d, T = 16, 2, 128, 16
+    P = Paged([20000, 300], T, Hkv, d, dtype, seed=3)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(2, Hq, d, generator=g).to(dtype).to(DEV)
+    qq = torch.randn(40, Hq, d, generator=g).to(dtype).to(DEV)
+    kv = torch.randn(2, Hkv, d, generator=g).to(dtype).to(DEV)
+    qs = torch.tensor([0, 30, 40], dtype=torch.int32, device=DEV)
+    cs = torch.rand(20000, d, generator=g).to(DEV)
+    side = torch.cuda.Stream()
+    u8 = torch.uint8
+    for call, shapes in (
+            (lambda s: E.paged_attn_decode(q, P.k, P.v, P.table, P.seq_len, 0.1, stream=s),
+             [((2, Hq, d), dtype), ((2, Hq), F32), ((E.paged_decode_workspace_bytes(Hq, Hkv, d),), u8)]),
+            (lambda s: E.paged_attn_prefill(qq, qs, P.k, P.v, P.table, P.seq_len, 0.1, stream=s),
+             [((40, Hq, d), dtype), ((40, Hq), F32), ((E.paged_prefill_workspace_bytes(40, 2, Hq, Hkv, d),), u8)]),
+            (lambda s: [E.paged_append(kv, kv, P.k, P.v, P.table, P.seq_len, q=q, cos_sin=cs, stream=s)],
+             [((2, Hq, d), dtype)])):
+        want = [x.clone() for x in call(None)]
+        got = _call_beside_pending_work(lambda: call(side), shapes)  # noqa: B023
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
