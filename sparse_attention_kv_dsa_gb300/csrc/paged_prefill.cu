@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(PS_THREADS, 2) paged_prefill_simt_kernel(const
       const int t0 = I.span.tile(it) * PS_KEYS;
       if (tid < PS_KEYS) {
         const int t = t0 + tid;
-        const bool some = t < I.len && t >= I.first && ((t >= I.lo && t < I.hi) || t < I.pre);
+        const bool own = I.holes ? seen_by_some(P, I, t0 + (tid & 32)) : t >= I.lo && t < I.hi;
+        const bool some = t < I.len && t >= I.first && (own || t < I.pre);
         S.row[tid] = some ? paged_row(P.C, I.b, t) : -1;
       }
       __syncthreads();

@@ -34,7 +34,7 @@
 //
 // Measured on a GB300 (cuBLAS bf16 1.94 PFLOP/s): a prompt of 8192, 64 heads of 128 over 8,
 // 0.91 ms, 1.2 PFLOP/s, bound by each tile's own round: 1500 cycles of softmax, 250 until the
-// last products start, 1000 to 1300 for them; 512 tokens over 32K, capped, 327 us, 0.83 PFLOP/s (a
+// last products start, 1000 to 1300 for them; 512 tokens over 32K, capped, 331 us, 0.82 PFLOP/s (a
 // softmax of 4000 cycles, with the polynomial tanh); 16 x 4 drafted tokens over 17K-20K, 207 us, 5.9 TB/s;
 // 8 packed prompts with documents and distance bias, 50 us, of which the plan, the first run of
 // the code and the joins are some 20.  Instruction fetch is part of every one of these figures:
@@ -352,6 +352,18 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
             const bool some = t < I.len && t >= I.first && ((t >= I.lo && t < I.hi) || t < I.pre);
             seen |= some ? 1u << k : 0u;
             ent[k] = some ? __ldg(C.page_table + (int64_t)I.b * C.max_pages + div_by(P.page, t)) : -1;
+          }
+          if (I.holes) {                                  // less what no row sees
+            uint32_t own = 0;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              const int t = t0 + lane + 32 * k;
+              own |= (seen_by_some(P, I, t0 + 32 * k) || t < I.pre) ? 1u << k : 0u;
+            }
+            seen &= own;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (!((seen >> k) & 1u)) ent[k] = -1;
           }
         }
         ok = ok && pt_wait(&S.uempty[e], ((x / PT_UNITS) & 1) ^ 1);

@@ -90,3 +90,60 @@ def test_default_buffers_on_a_given_stream_with_work_pending_on_the_current_one(
         want = [x.clone() for x in call(None)]
         got = _call_beside_pending_work(lambda: call(side), shapes)  # noqa: B023
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------ tokens that no row of a call sees --
+def _rows_first(kind, lens, new):
+    """First tokens of every row: rows of padding see nothing (their first token lies behind
+    them), the others see their document."""
+    first = []
+    for n, m in zip(lens, new):
+        for i, p in enumerate(range(n - m, n)):
+            if kind == "tail":                           # the last third of each sequence is padding
+                first.append(0x7fffffff if i >= m - m // 3 else 0)
+            elif kind == "documents":                    # documents of 23 tokens, padded to 32
+                first.append(n if p % 32 >= 23 else p // 32 * 32)
+            elif kind == "head":                         # the first rows are padding
+                first.append(p + 1 if i < m // 2 else max(0, p - 3))
+            else:                                        # a few rows here and there see something
+                first.append(max(0, p - 40) if i % 17 == 3 else p + 1 + i % 5)
+    return first
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq,Hkv,d,T", [(8, 2, 128, 16), (3, 3, 64, 5), (16, 1, 64, 8)])
+@pytest.mark.parametrize("kind", ["tail", "documents", "head", "sparse"])
+@pytest.mark.parametrize("kw", [dict(), dict(window=9), dict(prefix=(7, 0, 70)), dict(window=30, prefix=(0, 40, 1))])
+@pytest.mark.parametrize("lens,new", [([150, 9, 300], [150, 6, 120]), ([500, 40, 700], [7, 6, 8])])
+def test_prefill_tokens_that_no_row_sees_may_hold_anything(dtype, Hq, Hkv, d, T, kind, kw, lens, new):
+    """Padding tokens (below seq_len, but outside every row's sight) are NaN in the cache, and pages
+    that hold nothing else are not in the table: not an error, and no row's result."""
+    P = Paged(lens, T, Hkv, d, dtype, seed=11)
+    first, prefix, window = _rows_first(kind, lens, new), kw.get("prefix"), kw.get("window", 0)
+    table, r = P.table.clone(), 0
+    for b, (n, m) in enumerate(zip(lens, new)):
+        t, p = torch.arange(n), torch.arange(n - m, n)[:, None]
+        see = (t <= p) & (t > p - window if window else t >= 0)
+        if prefix:
+            see = see | (t < prefix[b])
+        see = (see & (t >= torch.tensor(first[r:r + m])[:, None])).any(0)
+        pg, row = P.at(b, t[~see])
+        P.k[pg, row], P.v[pg, row] = float("nan"), float("nan")
+        for i in range(-(-n // T)):
+            if not see[i * T:(i + 1) * T].any():
+                table[b, i] = -1
+        r += m
+    q = torch.randn(r, Hq, d, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    i32 = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    qs = i32([0, *torch.tensor(new).cumsum(0).tolist()])
+    out, lse = E.paged_attn_prefill(q, qs, P.k, P.v, table, P.seq_len, 0.1, window=window, first_tok=i32(first),
+                                    prefix_len=i32(prefix), status=P.status)
+    torch.cuda.synchronize()
+    assert P.status.item() == E.OK
+    r = 0
+    for b, (n, m) in enumerate(zip(lens, new)):
+        s = slice(r, r + m)
+        ref = attend(q[s].double().cpu(), P.K[b], P.V[b], range(n - m, n), 0.1, dtype=dtype, window=window,
+                     first=first[s], prefix=prefix[b] if prefix else 0)
+        check_rows(f"sequence {b}", out[s], lse[s], ref)
+        r += m
