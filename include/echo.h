@@ -647,8 +647,8 @@ typedef struct {
  *   ((t <= p and (window == 0 or t > p - window)) or t < prefix_len).
  */
 typedef struct {
-  float scale;
-  float softcap;              /* 0: none                                                  */
+  float scale;                /* finite, also as scale / softcap or scale * log2(e)       */
+  float softcap;              /* 0: none, or 1e-30 .. 1e30                                */
   const float *slopes;        /* [Hq] or NULL                                             */
   int32_t window;             /* 0: none                                                  */
   const int32_t *first_tok;   /* [N] per row (decode: [B]) first token seen (its document's

@@ -30,12 +30,6 @@ inline echo_status_t paged_check(const echo_paged_kv_t *c) {
   return ECHO_OK;
 }
 
-inline echo_status_t paged_scores_check(const echo_attn_scores_t *s) {
-  if (!s || !std::isfinite(s->scale) || !std::isfinite(s->softcap) || s->softcap < 0.f || s->window < 0)
-    return ECHO_ERR_INVALID_ARG;
-  return ECHO_OK;
-}
-
 // Rows of packed heads: 16-byte aligned, a whole number of 16-byte chunks apart.
 inline bool paged_rows_ok(const void *p, int64_t stride, int dtype) {
   return !((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * paged_elem_size(dtype))) & 15);
@@ -94,6 +88,16 @@ inline ScoreForm score_form(const echo_attn_scores_t *s) {
   f.c = s->softcap * kPgLog2e;
   return f;
 }
+
+// The form's factors have to be numbers that float32 holds: a finite (0 * inf is no score), c far
+// enough from both ends that a product flushed to 0 below 2^-126 is nothing beside it and that c
+// times a masked -inf stays one (c in the denormals reads as 0).
+inline echo_status_t paged_scores_check(const echo_attn_scores_t *s) {
+  if (!s || !std::isfinite(s->scale) || !std::isfinite(s->softcap) || s->window < 0) return ECHO_ERR_INVALID_ARG;
+  if (s->softcap != 0.f && !(s->softcap >= 1e-30f && s->softcap <= 1e30f)) return ECHO_ERR_INVALID_ARG;
+  return std::isfinite(score_form(s).a) ? ECHO_OK : ECHO_ERR_INVALID_ARG;
+}
+
 // 2^x, denormals as 0 (two units in the last place; half the cost of exp2f's full range).
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -147,3 +147,18 @@ def test_prefill_tokens_that_no_row_sees_may_hold_anything(dtype, Hq, Hkv, d, T,
                      first=first[s], prefix=prefix[b] if prefix else 0)
         check_rows(f"sequence {b}", out[s], lse[s], ref)
         r += m
+
+
+# ------------------------------------------------------------- the ends of the cap --
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale,cap", [(0.1, 1e30), (-0.3, 1e30), (0.1, 1e-30), (0.0, 1e-30)])
+def test_caps_at_both_ends_of_their_range(dtype, scale, cap):
+    # the largest cap leaves the scores as they are, the smallest makes them 0
+    P = Paged([300], 16, 2, 128, dtype)
+    q = torch.randn(40, 8, 128, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    qs = torch.tensor([0, 40], dtype=torch.int32, device=DEV)
+    ref = attend(q.double().cpu(), P.K[0], P.V[0], range(260, 300), scale if cap > 1 else 0.0, dtype=dtype)
+    out, lse = E.paged_attn_prefill(q, qs, P.k, P.v, P.table, P.seq_len, scale, softcap=cap)
+    check_rows("rows", out, lse, ref)
+    out, lse = E.paged_attn_decode(q[-1:], P.k, P.v, P.table, P.seq_len, scale, softcap=cap)
+    check_rows("token", out, lse, tuple(x[-1:] for x in ref))
