@@ -499,11 +499,14 @@ def _head_rows(t, N: int, d: int, dt, dev: int, where: str, name: str):
 
 
 def _attn_scores(scale, softcap, window, slopes, first_tok, prefix_len, rows: int, B: int, Hq: int, dev: int, where: str):
-    if slopes is first_tok is prefix_len is None:
-        return _SCORES.pack(scale, softcap, 0, window, 0, 0)
-    return _SCORES.pack(scale, softcap, _vec(slopes, Hq, _FL, dev, where, "slopes"), window,
-                        _vec(first_tok, rows, _INT, dev, where, "first_tok"),
-                        _vec(prefix_len, B, _INT, dev, where, "prefix_len"))
+    try:
+        if slopes is first_tok is prefix_len is None:
+            return _SCORES.pack(scale, softcap, 0, window, 0, 0)
+        return _SCORES.pack(scale, softcap, _vec(slopes, Hq, _FL, dev, where, "slopes"), window,
+                            _vec(first_tok, rows, _INT, dev, where, "first_tok"),
+                            _vec(prefix_len, B, _INT, dev, where, "prefix_len"))
+    except (struct.error, OverflowError):
+        _bad(where, "scale, softcap: float32 numbers; window: an int32")
 
 
 def _like(t, q, dt, shape, where: str, name: str):

@@ -162,3 +162,17 @@ def test_caps_at_both_ends_of_their_range(dtype, scale, cap):
     check_rows("rows", out, lse, ref)
     out, lse = E.paged_attn_decode(q[-1:], P.k, P.v, P.table, P.seq_len, scale, softcap=cap)
     check_rows("token", out, lse, tuple(x[-1:] for x in ref))
+
+
+# ----------------------------------------------------- numbers that no struct takes --
+@pytest.mark.parametrize("kw", [dict(window=1 << 31), dict(window=1 << 40), dict(scale=1e39), dict(softcap=1e300)])
+def test_numbers_past_the_structs_types_are_refused_like_others(kw):
+    P = Paged([20, 9], 8, 2, 64, BF)
+    q = torch.zeros(2, 4, 64, dtype=BF, device=DEV)
+    kw = dict(dict(scale=0.1), **kw)
+    qs = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    for call in (lambda: E.paged_attn_decode(q, P.k, P.v, P.table, P.seq_len, **kw),
+                 lambda: E.paged_attn_prefill(q, qs, P.k, P.v, P.table, P.seq_len, **kw)):
+        with pytest.raises(E.EchoError) as e:
+            call()
+        assert e.value.code == E.ERR_INVALID_ARG
