@@ -77,6 +77,7 @@ struct PtShared {
   int32_t page[PT_UNITS][PT_KEYS];
   int kvh[PT_UNITS], t0[PT_UNITS], whole[PT_UNITS];       // of a unit: KV head (-1: no more units), first token, every token there
   PlanShared plan;
+  uint64_t drain;                    // behind the rest: 8 bytes more ahead of the arrays cost a prompt 2 %
 };
 
 template <int D>
@@ -209,6 +210,20 @@ __device__ __forceinline__ uint32_t pt_bits(int a, int b) {
   return hi & ~lo;
 }
 
+// After a wait that gave up: the products in flight end (a bounded wait again), before their TMEM
+// is given back; the CTA's partials are not joined, and the call reports.
+static __device__ __noinline__ void pt_failed(uint64_t *drain, int32_t *rec, int32_t *status) {
+  const int warp = threadIdx.x >> 5;
+  if (warp == 11) {
+    if (pt_elect()) mma_commit(drain);
+    pt_wait(drain, 0);
+  }
+  if (threadIdx.x == 0) {
+    rec[0] = 0;
+    paged_fail(status, ECHO_ERR_TIMEOUT);
+  }
+}
+
 template <int D, int MOD, bool ALT>
 __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const __grid_constant__ PrefillParams P,
                                                                         const __grid_constant__ CUtensorMap kmap,
@@ -240,6 +255,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     for (int i = 0; i < PT_UNITS; ++i) { mbar_init(&S.ufull[i], 1); mbar_init(&S.uempty[i], 4); }
     for (int i = 0; i < PT_VM; ++i) S.vmtag[i] = 0;
     mbar_init(&S.mlfull, 128);
+    mbar_init(&S.drain, 1);
     S.fail = 0;
     fence_mbar_init();
   }
@@ -837,11 +853,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (S.fail) pt_failed(&S.drain, P.rec + blockIdx.x * 8, C.status);
   if (warp == 11) tmem_dealloc(tmem, 512);
-  if (S.fail && tid == 0) {
-    P.rec[blockIdx.x * 8] = 0;
-    paged_fail(C.status, ECHO_ERR_TIMEOUT);
-  }
 }
 
 // A bf16 tensor of `nd` dimensions with 128-byte-swizzled boxes of 64 innermost values; strides
