@@ -615,8 +615,11 @@ echo_status_t echo_expand_block_slots(const int32_t *sel_blk, const int32_t *blo
  * sequence b is row t % page_tokens of page page_table[b, t / page_tokens].
  *   - head_dim is 64 or 128, dtype ECHO_BF16 or ECHO_F32, page_tokens any positive number;
  *     k, v and every stride are multiples of 16 bytes.
- *   - seq_len[b] (device) counts sequence b's tokens with the new ones of the call; it is
- *     cut to [0, max_pages * page_tokens] (and INVALID_ARG set when it was not inside).
+ *   - seq_len[b] (device) counts sequence b's tokens with the new ones of the call.  The
+ *     attention calls cut it to [0, max_pages * page_tokens] (and set INVALID_ARG when it was
+ *     not inside); the append skips what lies outside (below).
+ *   - a call has a row and a sequence at least: N and B are positive (rows of sequences
+ *     without any, and rows behind the last sequence, are fine).
  *   - q_start [B+1] (device, q_start[0] = 0, not descending): sequence b's new tokens are
  *     rows q_start[b] .. q_start[b+1]-1 of the packed arrays; row i of n_b sits at position
  *     seq_len[b] - n_b + i.  Rows from q_start[B] on are left as they were.  Entries are
@@ -625,9 +628,9 @@ echo_status_t echo_expand_block_slots(const int32_t *sel_blk, const int32_t *blo
  *     positions that it names.
  *   - Only page-table entries of tokens that a call writes, or that some row of it sees,
  *     are used.  One outside [0, n_pages) sets ECHO_ERR_PAGE and its tokens are skipped.
- *     Rows of the pages that hold no token of the sequence (at or past seq_len) may hold
- *     anything, NaN too; keys and values below seq_len that some row of the call sees must
- *     be finite (one that one row sees may reach another row's result as 0 * NaN).
+ *     Rows of the pages that hold no token of the sequence (at or past seq_len), or one that
+ *     no row of the call sees, may hold anything, NaN too; keys and values that some row sees
+ *     must be finite (one that one row sees may reach another row's result as 0 * NaN).
  *   - status: optional device int32, sticky (first error wins), zeroed by the caller.
  */
 typedef struct {
@@ -689,6 +692,9 @@ echo_status_t echo_paged_append(const echo_paged_kv_t *cache, const void *q, int
 /*
  * Attention of one new token per sequence over a paged cache (grouped query heads: head i
  * reads KV head i / (Hq / n_kv_heads)).  The query of sequence b sits at seq_len[b] - 1.
+ * The cache is read once for each 16 query heads of a KV head (float32: 8).  From 32 heads to a
+ * KV head on, echo_paged_attn_prefill with one row a sequence (q_start 0, 1, .. B) measures
+ * faster: it packs up to 256 (float32: 64) rows of a KV head into a pass.
  *   out[b,i,:] = sum_t softmax_t(x) value_t;  lse[b,i] = log sum_t exp(x)   over seen t
  *   q [B, Hq, d] (q_stride values from row to row); out [B, Hq, d] contiguous, the cache's
  *   dtype; lse [B, Hq] float32; Hq / n_kv_heads a whole number up to 128.

@@ -106,7 +106,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float tanh_ex2(float u) { return 1.f - __fdividef(2.f, ex2(2.f * kPgLog2e * u) + 1.f); }
 // tanh(u) = u (1 + w (c1 + w (c2 + ...))), w = u^2 <= 1/2: minimax in relative error, found by an
-// exchange of extrema; 1.5e-8 off.
+// exchange of extrema; with the coefficients as float32 holds them 3.6e-8 off (at u = 0.683).
 constexpr float kTanhW = 0.5f;
 constexpr float kTanh1 = -0.3333311080932617f, kTanh2 = 0.13328056037425995f, kTanh3 = -0.05350292846560478f,
                 kTanh4 = 0.01996474526822567f, kTanh5 = -0.005034889094531536f;

@@ -3,8 +3,13 @@
 //   x_t = scale q . k_t, capped and biased;  out = sum_t e^(x_t) v_t / sum_t e^(x_t);
 //   lse = log sum_t e^(x_t)   over the tokens t that the query sees.
 //
-// Bound: every seen key and value is read once (4 d bytes a token and KV head in bf16)
-// for 4 G d operations, G query heads to a KV head: 16 operations a byte at most, so HBM.
+// Bound: a seen key and value (4 d bytes a token and KV head in bf16) is read once for each
+// group of 16 of its KV head's G query heads (8 in float32), 4 d operations a head: 16 operations
+// a byte at most, so HBM up to G = 16 (8).  More heads read the cache ceil(G / 16) (ceil(G / 8))
+// times, from L2 where the groups meet there.  16 sequences of 20K, one KV head of 128: bf16 68 us
+// at G = 16, 86 at 32, 132 at 64, 213 at 128; float32 136 at 8, 222 at 16, 1484 at 128.  The
+// many-token call with a row a sequence packs a KV head's heads and reads the cache once: bf16 68,
+// 69, 70, 75 us, float32 310 to 64 heads and 581 at 128.
 //
 // Split.  The cache is dealt out in units: tiles of TILE tokens of one KV head and up to ROWS
 // of its query heads, ordered by (sequence, KV head, tile).  A persistent grid computes from
@@ -26,10 +31,11 @@
 // for the scores, a lane to four values for the results.
 //
 // Measured on a GB300 (copy rate 6.78 TB/s): 16 sequences of 32K-48K tokens, 8 KV heads of 128
-// (2.63 GB) 396 us, 6.6 TB/s; 96 of up to 4K, 4 KV heads of 64, cap and window (552 MB) 103 us,
-// 5.4 TB/s, where the split's look-ups and its joining are some 15 us; 4 float32 sequences
-// (109 MB) 39 us; one of 8K (33.5 MB) 21 us, where two launches and the first run of either
-// kernel's code are most.  Not kept: a join of 512 threads a row, and one in a rolled loop with a
+// (2.63 GB) 386 to 397 us, 6.6 to 6.8 TB/s; 96 of up to 4K, 8 KV heads of 64, cap and window (552 MB)
+// 95 to 103 us, 5.4 to 5.8 TB/s; 4 float32 sequences (109 MB) 39 us; one of 8K (33.5 MB) 22 us, 17 a
+// call in a captured graph.  The join alone takes 7 to 11 us with cold caches, where its warps wait
+// for loads and for instructions (22 to 38 and 8 to 13 stalled warps an issue but for the 96
+// sequences, 11 and 2): most of what the short calls spend beside their bytes.  Not kept: a join of 512 threads a row, and one in a rolled loop with a
 // single load in flight (16 sequences 402 to 410 us); a third stage in place of the third CTA.
 
 #include "paged.cuh"
@@ -235,7 +241,7 @@ struct WarpBf {
       }
     }
     const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-    // weights, rounded to bf16 for the product (half a step, 2^-9 of each; the sums take the
+    // weights, rounded to bf16 for the product (by 2^-8 of each at most; the sums take the
     // unrounded ones)
 #pragma unroll
     for (int g = 0; g < TW / 16; ++g) {

@@ -228,8 +228,9 @@ static echo_status_t launch_simt(const PrefillParams &P, cudaStream_t st) {
 
 using namespace echo;
 
-// Two partials a CTA, of the rows of a row tile at most, and a record each: float32 has twice
-// the CTAs of bf16 and a quarter of the rows, so bf16's size holds both.
+// Two partials a CTA, of the rows of a row tile at most, and a record each.  Float32 has twice the
+// CTAs of bf16 and a quarter of the rows at most: the larger of the two holds both (with 64 packed
+// rows or fewer that is float32's).
 static int prefill_prows(int64_t N, int64_t G, int rows) { return (int)std::min<int64_t>(rows, N * G); }
 
 extern "C" size_t echo_paged_prefill_workspace_bytes(int32_t N, int32_t B, int32_t Hq, int32_t n_kv_heads, int32_t d) {

@@ -28,18 +28,20 @@
 // look-ups; warp 10: the queries; warps 12, 13: the keys; 14, 15: the values.  A tile of the
 // cache whose 128 tokens are all seen by some row comes by TMA, in boxes of the largest power of two of rows
 // that divides a page (8 or more, the period of the swizzle); the tiles at the ends of the
-// seen range, and pages that no box fits, by cp.async row by row, unseen tokens as zeros.  A
-// warp gets a TMA instruction away every 105 cycles whatever its box (measured), so two warps
-// share a tile: 16-row pages need 16 boxes of it.
+// seen range, and pages that no box fits, by cp.async row by row, unseen tokens as zeros.  Two
+// warps share a tile, as the issue of its boxes takes time whatever their size: 16-row pages need 16
+// of them.
 //
 // Measured on a GB300 (cuBLAS bf16 1.94 PFLOP/s): a prompt of 8192, 64 heads of 128 over 8,
-// 0.91 ms, 1.2 PFLOP/s, bound by each tile's own round: 1500 cycles of softmax, 250 until the
-// last products start, 1000 to 1300 for them; 512 tokens over 32K, capped, 331 us, 0.82 PFLOP/s (a
-// softmax of 4000 cycles, with the polynomial tanh); 16 x 4 drafted tokens over 17K-20K, 207 us, 5.9 TB/s;
-// 8 packed prompts with documents and distance bias, 50 us, of which the plan, the first run of
-// the code and the joins are some 20.  Instruction fetch is part of every one of these figures:
-// the issuing thread with its products unrolled for both tiles took 1000 and 347 us.  Handing P
-// over in two parts gains 25 us of the prompt and 3 of the capped chunk.  Not kept: 32-column stores of P, scores read from
+// 0.90 to 0.92 ms, 1.2 PFLOP/s; 512 tokens over 32K, capped, 331 us, 0.82 PFLOP/s; 16 x 4 drafted
+// tokens over 17K-20K, 204 to 208 us, 5.9 TB/s; 8 packed prompts with documents and distance bias,
+// 51 us, 48 a call in a captured graph.  No unit is full in the prompt (tensor 51 %, issue 50 %,
+// special functions 33 %, FMA 13 %) nor in the capped chunk (35, 46, 18, 25 %): a tile's product,
+// softmax and product follow one another, and two tiles in turn do not fill the gaps.  In the packed
+// prompts and the drafted tokens barriers of the plan (1.6 to 2.3 stalled warps an issue) and
+// missing instructions (0.8 to 1.5) count too.  The layout of the code and of PtShared moves the
+// prompt by percents: with the products unrolled for both tiles it took 1000 us (capped chunk 347).
+// Handing P over in two parts gains 25 us of the prompt and 3 of the capped chunk.  Not kept: 32-column stores of P, scores read from
 // TMEM twice in 32-column steps (1060 us rolled, 1131 unrolled; capped chunk 374 and 387), the
 // second half of the scores loaded under the first one's maximum (953 us, capped chunk 350).
 
@@ -118,17 +120,16 @@ __device__ __forceinline__ void pt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// One lane of the warp.  The compiler knows the branch for a single thread's: its TMA and MMA
-// instructions take their operands straight from uniform registers, where `lane == 0` made it
-// write a loop over the active lanes around each (an issue took some 100 cycles).
+// One lane of the warp, for the TMA and MMA instructions.  With it in place of `lane == 0`, rolled
+// waits, and TMA loads by a warp each, the prompt of 8192 went from 2.64 to 1.63 ms.
 __device__ __forceinline__ bool pt_elect() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// Bounded wait for a phase (a second from the 64th poll on).  Rolled up: this kernel has thirty
-// of them, and unrolled polls made it 223 KB, more than the instruction cache holds.  The
-// global timer is only read when the wait is long: it takes 200 cycles.
+// Bounded wait for a phase (a second from the 64th poll on).  Rolled up (see above), and the global
+// timer only read when the wait is long: that, two load warps a tile and a walk ahead of them took
+// the prompt of 8192 from 1.25 to 1.06 ms.
 __device__ __forceinline__ bool pt_wait1(uint64_t *bar, uint32_t parity) {
   uint64_t t0 = 0;
 #pragma unroll 1
@@ -641,8 +642,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
           tmem_wait_ld();
           if (CAP) {
             // u = s a, then tanh by its polynomial where every score of the warp is small enough
-            // (seven FMA-pipe operations, two scores each): the power and the reciprocal of the
-            // general form take 12 cycles of the special-function unit a score
+            // (seven operations of two scores each on the FMA units): the general form's power and
+            // reciprocal go through the special-function units (without it the capped chunk took 456 us)
             const uint64_t a2 = pt_pair(P.f.a, P.f.a);
             float um = 0.f;
 #pragma unroll
@@ -724,8 +725,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
             }
           }
           const float z = m == -INFINITY ? 0.f : m;
-          // weights, rounded to bf16 for the product (half a step, 2^-9 of each); the sum takes
-          // the unrounded ones
+          // weights, rounded to bf16 for the product (by 2^-8 of each at most); the sum takes the
+          // unrounded ones
           const uint64_t sc2 = pt_pair(sc, sc), z2 = pt_pair(-z, -z);
           uint64_t l2[4] = {0, 0, 0, 0};
 #pragma unroll
