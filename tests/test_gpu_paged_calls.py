@@ -176,3 +176,44 @@ def test_numbers_past_the_structs_types_are_refused_like_others(kw):
         with pytest.raises(E.EchoError) as e:
             call()
         assert e.value.code == E.ERR_INVALID_ARG
+
+
+# ------------------------------------------------ captured, with buffers of the call's own --
+@pytest.mark.parametrize("given", ["none", "same", "forked"])
+def test_captured_calls_with_default_buffers(given):
+    """Append, rows and token captured with buffers of their own, on the capturing stream, named or
+    not, or on one forked from it; replayed with other queries between other allocations."""
+    Hq, Hkv, d, T = 16, 2, 128, 16
+    P = Paged([5000, 300], T, Hkv, d, BF, seed=3)
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(2, h, d, generator=g).to(BF).to(DEV) for h in (Hq, Hkv, Hkv))
+    qq = torch.randn(40, Hq, d, generator=g).to(BF).to(DEV)
+    qs = torch.tensor([0, 30, 40], dtype=torch.int32, device=DEV)
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+    stream = {"none": None, "same": main, "forked": other}[given]
+
+    def calls(s):
+        r = E.paged_append(k, v, P.k, P.v, P.table, P.seq_len, q=q, stream=s)
+        a = E.paged_attn_prefill(qq, qs, P.k, P.v, P.table, P.seq_len, 0.1, stream=s)
+        return (*a, *E.paged_attn_decode(r, P.k, P.v, P.table, P.seq_len, 0.1, stream=s))
+
+    calls(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        if given == "forked":
+            other.wait_stream(main)
+        got = calls(stream)
+        if given == "forked":
+            main.wait_stream(other)
+    for i in range(4):
+        for x in (q, k, v, qq):
+            x.normal_()
+        want = [x.clone() for x in calls(None)]
+        for x in got:
+            x.fill_(7)
+        graph.replay()
+        junk = [torch.full((1 << 20,), 9.0, device=DEV) for _ in range(8)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+        del junk
