@@ -7,9 +7,8 @@ A case is one call.  `run` computes the plain form (elementary torch operations 
 rounded once) or, where `own` is true, calls the library.
 
 The quantised cache: a row (the d values of one token's key or value head) holds e4m3 codes
-and an exponent e in -15 .. 7, the smallest with max|x| <= 448 * 2^e if there is one; code =
-e4m3(x * 2^-e), saturating.  Every code * 2^e is a number of float16.  The exponents are held as
-float8_e8m0fnu, the number 2^e.
+and an exponent e in -64 .. 64, the smallest with max|x| <= 448 * 2^e; code = e4m3(x * 2^-e).
+The exponents are held as float8_e8m0fnu, the number 2^e.
 """
 
 import math
@@ -174,10 +173,10 @@ def work(case):
 
 # ------------------------------------------------------------- rows in 8 bits, plain --
 def _exponent(x):
-    """The exponent of rows x [..., d] (float32): max|x| <= 448 * 2^e, the smallest in -15 .. 7."""
+    """The exponent of rows x [..., d] (float32): max|x| <= 448 * 2^e, the smallest in -64 .. 64."""
     m, k = torch.frexp(x.abs().amax(-1))                                # max = m 2^k, 0.5 <= m < 1
     e = k - 9 + (m > 0.875).int()                                       # 448 = 0.875 * 2^9
-    return torch.where(m == 0, -15, e).clamp(-15, 7)
+    return torch.where(m == 0, -64, e).clamp(-64, 64)
 
 
 def _codes(x, e):
@@ -393,9 +392,9 @@ def _e4m3(x):
 def _rows_in_8(x):
     """Codes and numbers 2^e of rows x in float64, by trying the exponents from below."""
     top = x.abs().amax(-1)
-    e = torch.ceil(torch.log2(top.clamp(min=1e-30) / 448)).clamp(-15, 7)
+    e = torch.ceil(torch.log2(top.clamp(min=1e-30) / 448)).clamp(-64, 64)
     e = torch.where(top <= 448 * torch.exp2(e - 1), e - 1, e)
-    e = torch.where(top > 448 * torch.exp2(e), e + 1, e).clamp(-15, 7)
+    e = torch.where(top > 448 * torch.exp2(e), e + 1, e).clamp(-64, 64)
     return _e4m3((x * torch.exp2(-e)[..., None]).clamp(-448, 448)), torch.exp2(e)
 
 
