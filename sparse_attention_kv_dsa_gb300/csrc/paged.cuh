@@ -113,6 +113,18 @@ __device__ __forceinline__ void q8_halves(uint32_t w, uint32_t &lo, uint32_t &hi
       : "r"(w));
 }
 
+// 2^e, e an exponent of a row in 8 bits, as a pair of float16.
+__device__ __forceinline__ uint32_t q8_half_pow(int e) {
+  static_assert(kQ8MinExp == -15, "one exponent below float16's normal numbers");
+  const uint32_t h = e >= -14 ? (uint32_t)(15 + e) << 10 : 1u << 9;
+  return h | (h << 16);
+}
+__device__ __forceinline__ uint32_t q8_hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Scores in base-2 units: log2(e) * x of a raw product s = q . k.
 //   no cap:  s * a             with a = scale log2(e)
 //   cap:     c tanh(s a)       with a = scale / cap, c = cap log2(e)

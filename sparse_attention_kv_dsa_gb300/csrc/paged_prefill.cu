@@ -215,16 +215,17 @@ __global__ void __launch_bounds__(PS_THREADS, 2) paged_prefill_simt_kernel(const
   }
 }
 
-// A cache in 8 bits in bf16, page by page of the sequences' tables: each code times its power of two,
-// which bf16 holds exactly.  One byte read and two written a value: HBM.  A CTA takes pages in turn, a
+// A cache in 8 bits in 16 bits, page by page of the sequences' tables: each code times its power of two, keys in
+// bf16, for products with bf16 queries, values in float16, for products with float16 weights; either holds it
+// exactly.  One byte read and two written a value: HBM.  A CTA takes pages in turn, a
 // thread 16 codes at a time.  Rows at or past seq_len are left out, as are entries that are no page, which
 // stay none in the new table.
 constexpr int PQ_THREADS = 256;
 template <int D>
 __global__ void __launch_bounds__(PQ_THREADS) paged_q8_rows_kernel(const __grid_constant__ echo_paged_kv_t C,
                                                                    const __grid_constant__ echo_paged_scales_t X,
-                                                                   const int32_t *seq_len, int n, __nv_bfloat16 *k,
-                                                                   __nv_bfloat16 *v, int32_t *table) {
+                                                                   const int32_t *seq_len, int n, uint16_t *k,
+                                                                   uint16_t *v, int32_t *table) {
   constexpr int CH = D / 16;
   const int T = C.page_tokens, H = C.n_kv_heads;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
@@ -241,18 +242,25 @@ __global__ void __launch_bounds__(PQ_THREADS) paged_q8_rows_kernel(const __grid_
       const int64_t s = (int64_t)e * X.page_stride + (int64_t)t * X.row_stride + (int64_t)h * X.head_stride;
       const uint4 a[2] = {__ldg(reinterpret_cast<const uint4 *>((const uint8_t *)C.k + from)),
                           __ldg(reinterpret_cast<const uint4 *>((const uint8_t *)C.v + from))};
-      const float f[2] = {exp2i(q8_exp(__ldg(X.k + s))), exp2i(q8_exp(__ldg(X.v + s)))};
+      const float kf = exp2i(q8_exp(__ldg(X.k + s)));
+      const uint32_t vf = q8_half_pow(q8_exp(__ldg(X.v + s)));
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint32_t u[4] = {a[w].x, a[w].y, a[w].z, a[w].w};
         uint32_t o[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          uint32_t h2[2];
-          q8_halves(u[q >> 1], h2[0], h2[1]);
-          const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&h2[q & 1]));
-          const __nv_bfloat162 z = __floats2bfloat162_rn(y.x * f[w], y.y * f[w]);
-          o[q] = *reinterpret_cast<const uint32_t *>(&z);
+        for (int q = 0; q < 4; ++q) {
+          q8_halves(u[q], o[2 * q], o[2 * q + 1]);
+#pragma unroll
+          for (int z = 2 * q; z < 2 * q + 2; ++z) {
+            if (w) {
+              o[z] = q8_hmul2(o[z], vf);
+            } else {
+              const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&o[z]));
+              const __nv_bfloat162 b = __floats2bfloat162_rn(y.x * kf, y.y * kf);
+              o[z] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+          }
         }
         uint4 *dst = reinterpret_cast<uint4 *>((w ? v : k) + to + ((int64_t)h * T + t) * D + c * 16);
         dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -289,7 +297,7 @@ extern "C" size_t echo_paged_prefill_workspace_bytes(int32_t N, int32_t B, int32
   return (std::max(a, b) * (d + 2) + (size_t)PF_MAX_CTAS * 8) * sizeof(float);
 }
 
-// Where a cache in 8 bits is written out in bf16 first.  Turning a tile's codes costs the tensor-core kernel
+// Where a cache in 8 bits is written out in 16 bits first.  Turning a tile's codes costs the tensor-core kernel
 // some 0.7 us each time that a row tile reads it; writing them out and reading them back, 3 bytes a
 // value of HBM, is 2.5 us a tile, once.  A prompt of 8192, 64 heads over 8: 1430 us on the codes, 932 written
 // out first; 512 tokens over 32K, capped: 500 and 448
@@ -298,7 +306,7 @@ static bool q8_rows_first(int64_t N, int64_t B, int64_t G, int64_t bytes) {
   return N * G >= 4 * PF_MAX_ROWS * B && bytes <= (4ll << 30);
 }
 static size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
-// Keys (or values) of every page-table entry in bf16, and the table of where they lie.
+// Keys (or values) of every page-table entry in 16 bits, and the table of where they lie.
 static int64_t q8_rows_bytes(int64_t B, int64_t n_kv_heads, int64_t d, int64_t max_pages, int64_t page_tokens) {
   const double n = (double)B * max_pages * page_tokens * n_kv_heads * d * 2;
   return n < 1e15 ? (int64_t)n : (int64_t)1e15;
@@ -325,12 +333,12 @@ static echo_status_t launch_q8_rows(PrefillParams &P, unsigned char *at, cudaStr
   W.head_stride = (int64_t)C.page_tokens * C.head_dim;
   W.page_stride = W.head_stride * C.n_kv_heads;
   W.n_pages = P.B * C.max_pages;
-  W.dtype = ECHO_BF16;
+  W.dtype = ECHO_BF16;                                    // (16 bits a value)
   int32_t *table = reinterpret_cast<int32_t *>(at + 2 * rows);
   W.page_table = table;
   const dim3 grid(std::min(W.n_pages, 8 * sm_count()));
-  if (C.head_dim == 128) paged_q8_rows_kernel<128><<<grid, PQ_THREADS, 0, st>>>(C, P.X, P.seq_len, W.n_pages, (__nv_bfloat16 *)W.k, (__nv_bfloat16 *)W.v, table);
-  else paged_q8_rows_kernel<64><<<grid, PQ_THREADS, 0, st>>>(C, P.X, P.seq_len, W.n_pages, (__nv_bfloat16 *)W.k, (__nv_bfloat16 *)W.v, table);
+  if (C.head_dim == 128) paged_q8_rows_kernel<128><<<grid, PQ_THREADS, 0, st>>>(C, P.X, P.seq_len, W.n_pages, (uint16_t *)W.k, (uint16_t *)W.v, table);
+  else paged_q8_rows_kernel<64><<<grid, PQ_THREADS, 0, st>>>(C, P.X, P.seq_len, W.n_pages, (uint16_t *)W.k, (uint16_t *)W.v, table);
   ECHO_LAUNCH_OK();
   return ECHO_OK;
 }

@@ -367,6 +367,6 @@ __global__ void __launch_bounds__(128) paged_prefill_join_kernel(const __grid_co
 
 echo_status_t launch_prefill_tc(PrefillParams &P, cudaStream_t st);   // bf16
 echo_status_t launch_prefill_q8(PrefillParams &P, cudaStream_t st);   // e4m3 codes, bf16 queries
-echo_status_t launch_prefill_rows(PrefillParams &P, cudaStream_t st); // rows that were codes, in bf16
+echo_status_t launch_prefill_rows(PrefillParams &P, cudaStream_t st); // rows that were codes
 
 }  // namespace echo

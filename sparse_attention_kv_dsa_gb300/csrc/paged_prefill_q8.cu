@@ -5,16 +5,20 @@
 namespace echo {
 
 echo_status_t launch_prefill_q8(PrefillParams &P, cudaStream_t st) {
-  return P.C.head_dim == 128 ? launch_mod<128, true>(P, st) : launch_mod<64, true>(P, st);
+  return P.C.head_dim == 128 ? launch_mod<128, PT_CODES>(P, st) : launch_mod<64, PT_CODES>(P, st);
 }
 
-// Capped scores: as of codes.  (Rows are written out for 1024 rows a sequence or more: row tiles do not alternate.)
+// (Rows are written out for 1024 rows a sequence or more: row tiles do not alternate.)
 template <int D>
 static echo_status_t launch_rows(PrefillParams &P, cudaStream_t st) {
-  return P.slopes || P.f.a < 0.f ? launch_tc<D, 7, false, false>(P, st) : launch_tc<D, 5, false, false>(P, st);
+  switch ((P.f.capped ? 1 : 0) | (P.slopes || P.f.a < 0.f ? 2 : 0)) {
+    case 0: return launch_tc<D, 0, false, PT_WRITTEN>(P, st);
+    case 1: return launch_tc<D, 1, false, PT_WRITTEN>(P, st);
+    case 2: return launch_tc<D, 2, false, PT_WRITTEN>(P, st);
+    default: return launch_tc<D, 3, false, PT_WRITTEN>(P, st);
+  }
 }
 echo_status_t launch_prefill_rows(PrefillParams &P, cudaStream_t st) {
-  if (!P.f.capped) return launch_prefill_tc(P, st);
   return P.C.head_dim == 128 ? launch_rows<128>(P, st) : launch_rows<64>(P, st);
 }
 

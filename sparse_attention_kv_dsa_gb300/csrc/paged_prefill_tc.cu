@@ -5,7 +5,7 @@
 namespace echo {
 
 echo_status_t launch_prefill_tc(PrefillParams &P, cudaStream_t st) {
-  return P.C.head_dim == 128 ? launch_mod<128, false>(P, st) : launch_mod<64, false>(P, st);
+  return P.C.head_dim == 128 ? launch_mod<128, PT_BF16>(P, st) : launch_mod<64, PT_BF16>(P, st);
 }
 
 }  // namespace echo

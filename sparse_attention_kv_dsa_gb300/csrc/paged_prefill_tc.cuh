@@ -52,7 +52,7 @@
 // into zeros, and the softmax warps turn the queries, scaled by a power of two a row.  The weights,
 // 2^6 at the running maximum, go back as float16.  Turning a tile takes a warp some 1900 cycles, which shows:
 // 64 heads of 128 over 8, 128 tokens over 32K 166 us (128 with the cache in bf16), 512 over 32K 557 us (385).
-// Rows that many row tiles read are therefore written out in bf16 first (paged_prefill.cu), and a few rows a sequence go the
+// Rows that many row tiles read are therefore written out in 16 bits first (paged_prefill.cu; PT_WRITTEN), and a few rows a sequence go the
 // way of single tokens (paged_decode.cu); what is left for it are 33 to 1023 rows a sequence on
 // average, documents, and page tables too large to write out.  Code that is not small costs every warp
 // of the kernel (missing instructions: 1.9 stalled warps an issue against 0.5 in bf16).
@@ -71,7 +71,7 @@ constexpr int PT_UNITS = 4;          // ring of units looked up
 constexpr int PT_VM = 8;             // ring of the tiles' token masks
 constexpr int64_t kPtNone = INT64_MIN;   // row of a token that is not there
 constexpr uint32_t FMT_F16 = 0;      // of the products (FMT_BF16 is 1)
-constexpr int PT_Q8_UP = 6;          // e4m3: weights are 2^6 where they reach the running maximum
+constexpr int PT_H16_UP = 6;         // float16: weights are 2^6 where they reach the running maximum
 
 template <int D, bool ALT, bool Q8>
 struct PtShape {
@@ -111,9 +111,14 @@ struct PtQ8 {
   float qf[2][128];                  // of row tiles whose tiles alternate: the factors that undo the queries' scales
 };
 
-template <int D, bool ALT, bool Q8>
+// What a kernel reads: a bf16 cache, rows that were codes (keys in bf16, values in float16), or codes (Q8).  Of the
+// last two the weights are float16 (H16); of codes the queries too, which the softmax warps turn.  (Keys in
+// float16 too, and so queries that the softmax warps turn: a prompt of 8192, 64 heads over 8, 1235 us, 957 this way.)
+enum { PT_BF16, PT_WRITTEN, PT_CODES };
+
+template <int D, bool ALT, int IN>
 constexpr size_t pt_smem() {
-  return 1024 + (size_t)PtShape<D, ALT, Q8>::TILES + sizeof(PtShared) + (Q8 ? sizeof(PtQ8) : 0);
+  return 1024 + (size_t)PtShape<D, ALT, IN == PT_CODES>::TILES + sizeof(PtShared) + (IN == PT_CODES ? sizeof(PtQ8) : 0);
 }
 
 __device__ __forceinline__ void pt_cp_arrive(uint64_t *bar) {
@@ -248,17 +253,6 @@ __device__ __forceinline__ uint4 pt_lds(uint32_t a) {
 __device__ __forceinline__ void pt_sts(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// 2^e, e an exponent of a row in 8 bits, as a pair of float16.
-__device__ __forceinline__ uint32_t pt_half_pow(int e) {
-  static_assert(kQ8MinExp == -15, "one exponent below float16's normal numbers");
-  const uint32_t h = e >= -14 ? (uint32_t)(15 + e) << 10 : 1u << 9;
-  return h | (h << 16);
-}
-__device__ __forceinline__ uint32_t pt_hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // Sixteen codes to float16, times f, into two chunks of shared memory.
 __device__ __forceinline__ void pt_turn(const uint4 &w, uint32_t f, uint32_t to, uint32_t to1) {
   uint32_t h[8];
@@ -267,7 +261,7 @@ __device__ __forceinline__ void pt_turn(const uint4 &w, uint32_t f, uint32_t to,
   q8_halves(w.z, h[4], h[5]);
   q8_halves(w.w, h[6], h[7]);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) h[q] = pt_hmul2(h[q], f);
+  for (int q = 0; q < 8; ++q) h[q] = q8_hmul2(h[q], f);
   pt_sts(to, h[0], h[1], h[2], h[3]);
   pt_sts(to1, h[4], h[5], h[6], h[7]);
 }
@@ -296,22 +290,23 @@ static __device__ __noinline__ float pt_query(uint32_t tile, int r) {
   return exp2i(-up);
 }
 
-template <int D, int MOD, bool ALT, bool Q8>
+template <int D, int MOD, bool ALT, int IN>
 __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const __grid_constant__ PrefillParams P,
                                                                         const __grid_constant__ CUtensorMap kmap,
                                                                         const __grid_constant__ CUtensorMap vmap,
                                                                         const __grid_constant__ CUtensorMap qmap,
                                                                         int box, int qbox) {
+  constexpr bool Q8 = IN == PT_CODES, H16 = IN != PT_BF16;
   using Sh = PtShape<D, ALT, Q8>;
   constexpr int QB = Sh::QB, ATOMS = Sh::ATOMS, SLOTS = Sh::SLOTS, ROWS = Sh::ROWS, RING = ROWS / 128 * QB;
   // ring of codes: its tiles, where the first lies, from one to the next
   constexpr int RAW = Sh::INPLACE ? SLOTS : Sh::RAW ? Sh::RAW : 1, RAW0 = RING + (Sh::INPLACE ? QB / 2 : SLOTS * QB),
                 RAWB = Sh::INPLACE ? QB : 128 * D;
   constexpr bool CAP = MOD & 1, BIAS = MOD & 2;
-  // Tokens whose capped scores take one form of tanh.  Of a cache in 8 bits 32 (also MOD & 4: its rows in bf16; 512 rows over
+  // Tokens whose capped scores take one form of tanh.  Of a cache in 8 bits 32 (512 rows over
   // 32K with some scores past the polynomial 424 us a call, 447 with 128, 425 with 64 and 454 with 16), of
   // one in bf16 128, as its results have been.
-  constexpr int CAPN = Q8 || (MOD & 4) ? 32 : 128;
+  constexpr int CAPN = H16 ? 32 : 128;
   extern __shared__ unsigned char pt_raw[];
   unsigned char *R = pt_raw + ((0u - smem_u32(pt_raw)) & 1023u);    // (an offset: it stays a pointer to shared memory)
   PtShared &S = *reinterpret_cast<PtShared *>(R + Sh::TILES);
@@ -403,7 +398,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
         const bool whole = S.whole[e];
         asm volatile("" : "+r"(byte[0]), "+r"(byte[1])::"memory");             // (no use of them moves up to their loads)
         // 0: the row's token is not there, or seen by none: whatever its place holds reads as zeros
-        const uint32_t f0 = byte[0] < 256 ? pt_half_pow(q8_exp(byte[0])) : 0, f1 = byte[1] < 256 ? pt_half_pow(q8_exp(byte[1])) : 0;
+        const uint32_t f0 = byte[0] < 256 ? q8_half_pow(q8_exp(byte[0])) : 0, f1 = byte[1] < 256 ? q8_half_pow(q8_exp(byte[1])) : 0;
         exponents(x + 1);
         if (!ok) break;
         if (!(Sh::INPLACE && box) && !pt_wait(&S.empty[sl], ((g / SLOTS) & 1) ^ 1)) { ok = false; break; }
@@ -689,9 +684,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       // stalls until the products before it are done, so there is one a QK, and what else it
       // sets free -- K(x), V(x - 1), a row tile's queries -- the softmax warps hand back when
       // they wake up on it.
-      constexpr uint32_t FMT = Q8 ? FMT_F16 : FMT_BF16;
-      constexpr uint32_t id_qk = instr_desc(FMT, FMT, 0, 0, 128, 128);
-      constexpr uint32_t id_pv = instr_desc(FMT, FMT, 0, 1, 128, D);
+      constexpr uint32_t QK = Q8 ? FMT_F16 : FMT_BF16, PV = H16 ? FMT_F16 : FMT_BF16;
+      constexpr uint32_t id_qk = instr_desc(QK, QK, 0, 0, 128, 128);
+      constexpr uint32_t id_pv = instr_desc(PV, PV, 0, 1, 128, D);
       const uint32_t ring = smem_u32(R + RING);
       const uint64_t qd = smem_desc(smem_u32(R), 16, 1024, LAYOUT_SW128);
       const uint64_t kd = smem_desc(ring, 16, 1024, LAYOUT_SW128);
@@ -972,8 +967,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
               pt_st16(to + k, o);
             }
           }
-          const float z = m == -INFINITY ? 0.f : Q8 ? m - (float)PT_Q8_UP : m;
-          // weights, rounded to bf16 (float16) for the product (by 2^-9, 2^-12 of each at most); the sum takes the
+          const float z = m == -INFINITY ? 0.f : H16 ? m - (float)PT_H16_UP : m;
+          // weights, rounded to bf16 (float16) for the product (by 2^-8, 2^-11 of each at most); the sum takes the
           // unrounded ones
           const uint64_t sc2 = pt_pair(sc, sc), z2 = pt_pair(-z, -z);
           uint64_t l2[4] = {0, 0, 0, 0};
@@ -987,7 +982,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
               a = ex2(a);
               c = ex2(c);
               l2[(q >> 1) & 3] = pt_add2(l2[(q >> 1) & 3], pt_pair(a, c));
-              if (Q8) {
+              if (H16) {
                 asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[q >> 1]) : "f"(c), "f"(a));
               } else {
                 const __nv_bfloat162 h = __floats2bfloat162_rn(a, c);
@@ -1100,7 +1095,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
       mbar_arrive(&S.oempty[t]);
       if (alt) mbar_arrive(&S.oempty[1]);
       if (there) {
-        const float m1 = Q8 ? m - (float)PT_Q8_UP : m;
+        const float m1 = H16 ? m - (float)PT_H16_UP : m;
         if (done) P.lse[orow] = l == 0.f ? -INFINITY : (m1 + log2f(l)) * kPgLn2;
         else *reinterpret_cast<float2 *>(P.pml + prow * 2) = make_float2(m1, l);
       }
@@ -1117,10 +1112,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
   if (warp == 11) tmem_dealloc(tmem, 512);
 }
 
-template <int D, int MOD, bool ALT, bool Q8>
+template <int D, int MOD, bool ALT, int IN>
 static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
-  static_assert(pt_smem<D, ALT, Q8>() <= 227 * 1024, "fits an SM");
-  ECHO_CUDA_OK((allow_smem<paged_prefill_tc_kernel<D, MOD, ALT, Q8>>(pt_smem<D, ALT, Q8>())));
+  constexpr bool Q8 = IN == PT_CODES;
+  constexpr size_t smem = pt_smem<D, ALT, IN>();
+  static_assert(smem <= 227 * 1024, "fits an SM");
+  ECHO_CUDA_OK((allow_smem<paged_prefill_tc_kernel<D, MOD, ALT, IN>>(smem)));
   int box = std::min(P.C.page_tokens & -P.C.page_tokens, PT_KEYS);
   int qbox = !Q8 && 128 % P.G == 0 ? 128 / P.G : 0;
   CUtensorMap kmap = {}, vmap = {}, qmap = {};
@@ -1140,13 +1137,13 @@ static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
     if (qbox && !pg_map(&qmap, P.q, ECHO_BF16, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B)) qbox = 0;
   }
   const int grid = std::min(sm_count(), PF_MAX_CTAS / 2);
-  paged_prefill_tc_kernel<D, MOD, ALT, Q8><<<grid, PT_THREADS, pt_smem<D, ALT, Q8>(), st>>>(P, kmap, vmap, qmap, box, qbox);
+  paged_prefill_tc_kernel<D, MOD, ALT, IN><<<grid, PT_THREADS, smem, st>>>(P, kmap, vmap, qmap, box, qbox);
   ECHO_LAUNCH_OK();
   ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<__nv_bfloat16, D>, dim3(grid, (P.prows + 3) / 4), dim3(128), st, P));
   return ECHO_OK;
 }
 
-template <int D, bool Q8>
+template <int D, int IN>
 static echo_status_t launch_mod(PrefillParams &P, cudaStream_t st) {
   // a negative scale goes with the bias: the plain form takes the largest raw product
   const int mod = (P.f.capped ? 1 : 0) | (P.slopes || P.f.a < 0.f ? 2 : 0);
@@ -1156,14 +1153,14 @@ static echo_status_t launch_mod(PrefillParams &P, cudaStream_t st) {
   // query tile; either kernel is right for any mixture.
   const bool alt = (int64_t)P.N * P.G <= 128 * (int64_t)P.B;
   switch (2 * mod + (alt ? 1 : 0)) {
-    case 0: return launch_tc<D, 0, false, Q8>(P, st);
-    case 1: return launch_tc<D, 0, true, Q8>(P, st);
-    case 2: return launch_tc<D, 1, false, Q8>(P, st);
-    case 3: return launch_tc<D, 1, true, Q8>(P, st);
-    case 4: return launch_tc<D, 2, false, Q8>(P, st);
-    case 5: return launch_tc<D, 2, true, Q8>(P, st);
-    case 6: return launch_tc<D, 3, false, Q8>(P, st);
-    default: return launch_tc<D, 3, true, Q8>(P, st);
+    case 0: return launch_tc<D, 0, false, IN>(P, st);
+    case 1: return launch_tc<D, 0, true, IN>(P, st);
+    case 2: return launch_tc<D, 1, false, IN>(P, st);
+    case 3: return launch_tc<D, 1, true, IN>(P, st);
+    case 4: return launch_tc<D, 2, false, IN>(P, st);
+    case 5: return launch_tc<D, 2, true, IN>(P, st);
+    case 6: return launch_tc<D, 3, false, IN>(P, st);
+    default: return launch_tc<D, 3, true, IN>(P, st);
   }
 }
 
