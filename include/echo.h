@@ -790,9 +790,10 @@ echo_status_t echo_paged_append_q8(const echo_paged_kv_t *cache, const echo_page
  * echo_paged_attn_decode and echo_paged_attn_prefill over a cache in 8 bits; the same masks,
  * limits and errors (and TIMEOUT, from either), with bf16 q and out.  echo_paged_attn_decode_q8 takes echo_paged_attn_decode's
  * workspace.  echo_paged_attn_prefill_q8 works on the codes themselves with echo_paged_attn_prefill's; with
- * echo_paged_prefill_q8_workspace_bytes it writes the sequences' rows out in 16 bits first (exactly) where
- * every one of them is read by many rows: four tiles of 256 packed rows a sequence or more on average, and a
- * page table that bounds what is written by 4 GiB.  Otherwise the two sizes are the same.
+ * echo_paged_prefill_q8_workspace_bytes it writes the tokens that a sequence's rows see (from the smallest lower end of
+ * them on, and by a prefix) out in 16 bits first, exactly, where packed rows are many: 1024 (token, query head of a KV
+ * head) pairs a sequence or more on average over N and B, and a page table whose max_pages * page_tokens bound
+ * what could be written by 4 GiB (the workspace's size goes by them).  Otherwise the two sizes are the same.
  * The codes are not rounded again.  Scores are float32 sums of products of codes and a query, which is scaled
  * by a power of two to float16 (exact where it is above 2^-31 of its head's largest value); weights are
  * rounded to float16, and those below 2^-31 of a row's largest may be lost.  Codes and exponents of tokens that no row sees may be anything.

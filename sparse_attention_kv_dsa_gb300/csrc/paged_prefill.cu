@@ -217,27 +217,66 @@ __global__ void __launch_bounds__(PS_THREADS, 2) paged_prefill_simt_kernel(const
 
 // A cache in 8 bits in 16 bits, page by page of the sequences' tables: each code times its power of two, keys in
 // bf16, for products with bf16 queries, values in float16, for products with float16 weights; either holds it
-// exactly.  One byte read and two written a value: HBM.  A CTA takes pages in turn, a
-// thread 16 codes at a time.  Rows at or past seq_len are left out, as are entries that are no page, which
-// stay none in the new table.
+// exactly.  One byte read and two written a value: HBM.  A CTA takes pages in turn, a thread 16 codes at a time.
+// Of a sequence the tokens that its rows see are written, [first, pre) by a prefix and [lo, len) from the smallest
+// lower end on; the others' places are left alone (512 rows under a window of 512 at 128K
+// tokens 178 -> 43 us).  Entries that are no page stay none in
+// the new table.
 constexpr int PQ_THREADS = 256;
+struct SeenTokens {
+  int first, pre, lo, len;           // (pre <= lo: what a prefix adds)
+};
+// The whole block calls it.
+__device__ __forceinline__ SeenTokens seen_tokens(const PrefillParams &P, int b) {
+  __shared__ int red[2][PQ_THREADS / 32];
+  const SeqRows R = seq_rows(P, b);
+  SeenTokens s;
+  s.len = min(max(__ldg(P.seq_len + b), 0), P.C.max_pages * P.C.page_tokens);
+  const int p0 = s.len - R.n, i0 = max(0, -p0);           // rows at positions >= 0
+  if (i0 >= R.n) return {0, 0, 0, 0};
+  s.first = 0;
+  s.lo = P.window ? max(0, p0 + i0 - P.window + 1) : 0;
+  if (P.first_tok) {
+    int f = 0x7fffffff, l = 0x7fffffff;
+#pragma unroll 4
+    for (int i = i0 + (int)threadIdx.x; i < R.n; i += PQ_THREADS) {
+      const int g = max(__ldg(P.first_tok + R.s0 + i), 0);
+      f = min(f, g);
+      l = min(l, P.window ? max(g, p0 + i - P.window + 1) : g);
+    }
+    f = __reduce_min_sync(0xffffffffu, f);
+    l = __reduce_min_sync(0xffffffffu, l);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = f, red[1][threadIdx.x >> 5] = l;
+    __syncthreads();
+    s.first = __reduce_min_sync(0xffffffffu, red[0][threadIdx.x & (PQ_THREADS / 32 - 1)]);
+    s.lo = __reduce_min_sync(0xffffffffu, red[1][threadIdx.x & (PQ_THREADS / 32 - 1)]);
+  }
+  s.pre = P.prefix_len ? min(min(__ldg(P.prefix_len + b), s.len), s.lo) : 0;
+  return s;
+}
 template <int D>
-__global__ void __launch_bounds__(PQ_THREADS) paged_q8_rows_kernel(const __grid_constant__ echo_paged_kv_t C,
-                                                                   const __grid_constant__ echo_paged_scales_t X,
-                                                                   const int32_t *seq_len, int n, uint16_t *k,
+__global__ void __launch_bounds__(PQ_THREADS) paged_q8_rows_kernel(const __grid_constant__ PrefillParams P, int n, uint16_t *k,
                                                                    uint16_t *v, int32_t *table) {
   constexpr int CH = D / 16;
+  const echo_paged_kv_t &C = P.C;
+  const echo_paged_scales_t &X = P.X;
   const int T = C.page_tokens, H = C.n_kv_heads;
+  SeenTokens S = {};
+  int of = -1;                                            // the sequence that S is of
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const int b = i / C.max_pages, p = i - b * C.max_pages;
-    const int32_t e = __ldg(C.page_table + i);
-    const int64_t left = (int64_t)min(max(__ldg(seq_len + b), 0), C.max_pages * T) - (int64_t)p * T;
+    const int b = i / C.max_pages, p0 = (i - b * C.max_pages) * T;
+    const int32_t e = __ldg(C.page_table + i);            // (on its way under the look at first tokens)
+    if (b != of) S = seen_tokens(P, of = b);
+    const int a0 = max(p0, S.first), a1 = min(p0 + T, S.pre), b0 = max(p0, S.lo), b1 = min(p0 + T, S.len);
+    if (a0 >= a1 && b0 >= b1) continue;
     const bool page = e >= 0 && e < C.n_pages;
     if (threadIdx.x == 0) table[i] = page ? i : -1;
-    if (!page || left <= 0) continue;
-    const int64_t rows = (left < T ? left : T) * H, to = (int64_t)i * T * H * D;
-    for (int64_t x = threadIdx.x; x < rows * CH; x += PQ_THREADS) {
-      const int c = (int)(x % CH), h = (int)(x / CH % H), t = (int)(x / CH / H);
+    if (!page) continue;
+    const int64_t to = (int64_t)i * T * H * D;
+    const int na = max(a1 - a0, 0), nr = na + max(b1 - b0, 0);
+    for (int64_t x = threadIdx.x; x < (int64_t)nr * H * CH; x += PQ_THREADS) {
+      const int c = (int)(x % CH), h = (int)(x / CH % H), y = (int)(x / CH / H), t = (y < na ? a0 + y : b0 + (y - na)) - p0;
       const int64_t from = (int64_t)e * C.page_stride + (int64_t)t * C.row_stride + (int64_t)h * C.head_stride + c * 16;
       const int64_t s = (int64_t)e * X.page_stride + (int64_t)t * X.row_stride + (int64_t)h * X.head_stride;
       const uint4 a[2] = {__ldg(reinterpret_cast<const uint4 *>((const uint8_t *)C.k + from)),
@@ -300,8 +339,7 @@ extern "C" size_t echo_paged_prefill_workspace_bytes(int32_t N, int32_t B, int32
 // Where a cache in 8 bits is written out in 16 bits first.  Turning a tile's codes costs the tensor-core kernel
 // some 0.7 us each time that a row tile reads it; writing them out and reading them back, 3 bytes a
 // value of HBM, is 2.5 us a tile, once.  A prompt of 8192, 64 heads over 8: 1430 us on the codes, 932 written
-// out first; 512 tokens over 32K, capped: 500 and 448
-// (424 since).
+// out first; 512 tokens over 32K, capped: 500 and 448 (424 since).
 static bool q8_rows_first(int64_t N, int64_t B, int64_t G, int64_t bytes) {
   return N * G >= 4 * PF_MAX_ROWS * B && bytes <= (4ll << 30);
 }
@@ -324,7 +362,8 @@ extern "C" size_t echo_paged_prefill_q8_workspace_bytes(int32_t N, int32_t B, in
 // Writes the cache's rows out and points P at them: pages of the same tokens, heads first, entry (b, p) at
 // b * max_pages + p.
 static echo_status_t launch_q8_rows(PrefillParams &P, unsigned char *at, cudaStream_t st) {
-  const echo_paged_kv_t C = P.C;
+  const PrefillParams R = P;
+  const echo_paged_kv_t &C = R.C;
   const size_t rows = round256((size_t)q8_rows_bytes(P.B, C.n_kv_heads, C.head_dim, C.max_pages, C.page_tokens));
   echo_paged_kv_t &W = P.C;
   W.k = at;
@@ -337,8 +376,8 @@ static echo_status_t launch_q8_rows(PrefillParams &P, unsigned char *at, cudaStr
   int32_t *table = reinterpret_cast<int32_t *>(at + 2 * rows);
   W.page_table = table;
   const dim3 grid(std::min(W.n_pages, 8 * sm_count()));
-  if (C.head_dim == 128) paged_q8_rows_kernel<128><<<grid, PQ_THREADS, 0, st>>>(C, P.X, P.seq_len, W.n_pages, (uint16_t *)W.k, (uint16_t *)W.v, table);
-  else paged_q8_rows_kernel<64><<<grid, PQ_THREADS, 0, st>>>(C, P.X, P.seq_len, W.n_pages, (uint16_t *)W.k, (uint16_t *)W.v, table);
+  if (C.head_dim == 128) paged_q8_rows_kernel<128><<<grid, PQ_THREADS, 0, st>>>(R, W.n_pages, (uint16_t *)W.k, (uint16_t *)W.v, table);
+  else paged_q8_rows_kernel<64><<<grid, PQ_THREADS, 0, st>>>(R, W.n_pages, (uint16_t *)W.k, (uint16_t *)W.v, table);
   ECHO_LAUNCH_OK();
   return ECHO_OK;
 }

@@ -7,7 +7,7 @@ import torch
 import sparse_attention_kv_dsa_gb300.echo as E
 
 from paged_q8_ref import F8, PagedQ8, attend_q8
-from paged_ref import DEV, half_step
+from paged_ref import DEV, check_rows, half_step
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -52,3 +52,39 @@ def test_default_workspace_keeps_float16_weights(d, Hq, Hkv, lens, new, cap, ali
         assert worst <= 0, f"sequence {b}: {worst} past the bound"
         assert torch.all((lse[s].double().cpu() - wlse).abs() <= ltol)
         r += n
+
+
+@pytest.mark.parametrize("kw", [dict(window=64), dict(window=64, prefix=40), dict(window=300, first=19700), dict(first=19500),
+                                dict(first=19500, prefix=19530), dict(window=1)])
+@pytest.mark.parametrize("T,d", [(16, 128), (24, 64), (1000, 64)])
+def test_only_tokens_that_a_row_sees_are_written_out(T, d, kw):
+    """Many rows at the end of a long cache that see a few of its tokens: the others are not read (NaN codes under a NaN
+    exponent, no page for most) and leave their places in the workspace alone."""
+    L, n, Hq, Hkv, u8 = 20000, 200, 16, 2, torch.uint8
+    P = PagedQ8([L], T, Hkv, d, seed=T)
+    first, window, prefix = kw.get("first"), kw.get("window", 0), kw.get("prefix", 0)
+    t, p = torch.arange(L), torch.arange(L - n, L)[:, None]
+    see = (t <= p) & (t > p - window if window else t >= 0) | (t < prefix)
+    see = (see & (t >= (first or 0))).any(0)
+    pg, row = P.at(0, t[~see])
+    for pool, x in ((P.kc, 0x7f), (P.vc, 0xff), (P.ke, 255), (P.ve, 255)):
+        pool[pg, row] = x
+    table = P.table.clone()
+    for i in range(-(-L // T)):
+        if not see[i * T:(i + 1) * T].any():
+            table[0, i] = -1
+    q = (torch.randn(n, Hq, d, generator=torch.Generator().manual_seed(1)) * 0.1).to(BF).to(DEV)
+    first_tok = None if first is None else torch.full((n,), first, dtype=torch.int32, device=DEV)
+    small = -(-E.paged_prefill_workspace_bytes(n, 1, Hq, Hkv, d) // 256) * 256
+    ws = torch.full((E.paged_prefill_q8_workspace_bytes(n, 1, Hq, Hkv, d, table.shape[1], T),), 0xa5, dtype=u8, device=DEV)
+    rows = 2 * (-(-table.shape[1] * T * Hkv * d * 2 // 256) * 256)
+    assert ws.numel() >= small + rows
+    out, lse = E.paged_attn_prefill(q, starts([n]), *P.pages, table, P.seq_len, 0.1, window=window, first_tok=first_tok,
+                                    prefix_len=torch.tensor([prefix], dtype=torch.int32, device=DEV) if prefix else None,
+                                    workspace=ws, status=P.status, **P.scales)
+    torch.cuda.synchronize()
+    assert P.status.item() == E.OK
+    check_rows("rows", out, lse, attend_q8(q.double().cpu(), P.K[0], P.V[0], P.VE[0], torch.arange(L - n, L), 0.1, window=window,
+                                           first=None if first is None else [first] * n, prefix=prefix))
+    written = int((ws[small:small + rows] != 0xa5).sum())
+    assert 0.9 <= written / (int(see.sum()) * Hkv * d * 2 * 2) <= 1
