@@ -341,7 +341,7 @@ extern "C" size_t echo_paged_prefill_workspace_bytes(int32_t N, int32_t B, int32
 // value of HBM, is 2.5 us a tile, once.  A prompt of 8192, 64 heads over 8: 1430 us on the codes, 932 written
 // out first; 512 tokens over 32K, capped: 500 and 448 (424 since).
 static bool q8_rows_first(int64_t N, int64_t B, int64_t G, int64_t bytes) {
-  return N * G >= 4 * PF_MAX_ROWS * B && bytes <= (4ll << 30);
+  return N * G >= 4 * PF_MAX_ROWS * B && bytes <= (1ll << 30);
 }
 static size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Keys (or values) of every page-table entry in 16 bits, and the table of where they lie.

@@ -88,3 +88,10 @@ def test_only_tokens_that_a_row_sees_are_written_out(T, d, kw):
                                            first=None if first is None else [first] * n, prefix=prefix))
     written = int((ws[small:small + rows] != 0xa5).sum())
     assert 0.9 <= written / (int(see.sum()) * Hkv * d * 2 * 2) <= 1
+
+
+def test_rows_written_out_stay_below_a_gibibyte():
+    base = E.paged_prefill_workspace_bytes(8192, 1, 64, 8, 128)
+    for tokens, more in ((16, True), (1 << 18, True), ((1 << 18) + 16, False), (1 << 20, False)):
+        size = E.paged_prefill_q8_workspace_bytes(8192, 1, 64, 8, 128, tokens // 16, 16)
+        assert (size > base) == more and size <= base + 512 + (1 << 30) + tokens // 4
