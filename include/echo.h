@@ -793,7 +793,9 @@ echo_status_t echo_paged_append_q8(const echo_paged_kv_t *cache, const echo_page
  * echo_paged_prefill_q8_workspace_bytes it writes the tokens that a sequence's rows see (from the smallest lower end of
  * them on, and by a prefix) out in 16 bits first, exactly, where packed rows are many: 1024 (token, query head of a KV
  * head) pairs a sequence or more on average over N and B, and a page table whose max_pages * page_tokens bound
- * what could be written by 1 GiB (the workspace's size goes by them).  Otherwise the two sizes are the same.
+ * what could be written by 1 GiB (the workspace's size goes by them).  Otherwise the two sizes are the same.  Where N
+ * packed rows are 32 a sequence or fewer on average and first_tok is NULL, sequences with 32 at most take
+ * echo_paged_attn_decode_q8's way, in calls of up to 1024 rows those with more too.
  * The codes are not rounded again.  Scores are float32 sums of products of codes and a query, which is scaled
  * by a power of two to float16 (exact where it is above 2^-31 of its head's largest value); weights are
  * rounded to float16, and those below 2^-31 of a row's largest may be lost.  Codes and exponents of tokens that no row sees may be anything.

@@ -192,10 +192,11 @@ inline cudaError_t allow_smem(size_t bytes) {
 // Launches K so that it may start up while the kernel before it in the stream ends; K itself
 // waits for it (griddepcontrol.wait) before it reads what that kernel wrote.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_after(void (*K)(KArgs...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+inline cudaError_t launch_after(void (*K)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -227,11 +228,16 @@ __device__ __forceinline__ TileSpan tile_span(int first, int pre, int lo, int hi
   return s;
 }
 
+// The many-token call's workspace: records of split row tiles (PF_MAX_CTAS of 8 int32), then partials.  Of a call
+// over codes the last record, which no CTA has, tells whether some sequence has more than a few rows.
+constexpr int kPgRecords = 8 * 320, kPgSomeAt = kPgRecords - 8;
+
 // Attention of a few new tokens a sequence over a cache in 8 bits (paged_decode.cu): whether a many-token
-// call is one, and the call (its arguments checked).
+// call is one, and the call (its arguments checked), which leaves out sequences of more than `most` packed rows
+// and notes in the workspace whether there are any (not if q_start descends, which it reports).
 bool few_tokens_q8(int64_t N, int64_t B, int64_t G, const echo_attn_scores_t *scores);
 echo_status_t launch_few_tokens_q8(const echo_paged_kv_t *cache, const echo_paged_scales_t *scales, const void *q, int64_t q_stride,
                                    const int32_t *q_start, const int32_t *seq_len, int32_t N, int32_t B, int32_t Hq,
-                                   const echo_attn_scores_t *scores_of, void *out, float *lse, void *workspace, cudaStream_t st);
+                                   const echo_attn_scores_t *scores_of, int most, void *out, float *lse, void *workspace, cudaStream_t st);
 
 }  // namespace echo

@@ -90,7 +90,8 @@ struct DecodeParams {
   int whole;                         // e4m3: every (sequence, KV head, group) is one CTA's, none is split
   // several new tokens a sequence (MULTI): rows q_start[b] .. of sequence b, of N; G FastDiv'ed
   const int32_t *q_start;
-  int N;
+  int N, most;                       // sequences of more packed rows than `most` are left out, *some: there are any
+  int32_t *some;
   FastDiv group;
 };
 
@@ -135,7 +136,8 @@ struct DecodeSpan {
 // MULTI: of a sequence's new tokens, the rows [s0, s0 + n) of the packed arrays.
 __device__ __forceinline__ int decode_rows(const DecodeParams &P, int b, int &s0) {
   s0 = min(max(P.q_start[b], 0), P.N);
-  return max(min(max(P.q_start[b + 1], 0), P.N) - s0, 0);
+  const int n = max(min(max(P.q_start[b + 1], 0), P.N) - s0, 0);
+  return (int64_t)n * P.G <= P.most ? n : 0;
 }
 template <bool MULTI = false>
 __device__ __forceinline__ DecodeSpan decode_span(const DecodeParams &P, int b, int tile, int rows = 1) {
@@ -875,7 +877,7 @@ __global__ void __launch_bounds__(PdShape<T, D, NT, MULTI>::THREADS, PdShape<T, 
   // scan gives the total and finds the place.  Whether it is found is known from the barrier behind
   // the writes of S.seq and S.before, the same in every thread: nobody reads either ahead of it
   uint32_t total = 0, end = 0, n = 0, per = 0, u0 = 0, u1 = 0;
-  bool found = false, bad = false;
+  bool found = false, bad = false, some = false;
   if (tid == 0) P.rec[blockIdx.x * 4] = 0;
   if (Sh::Q8) {
     if (tid == 0) {
@@ -894,7 +896,11 @@ __global__ void __launch_bounds__(PdShape<T, D, NT, MULTI>::THREADS, PdShape<T, 
     for (int b0 = 0; b0 < P.B && !found; b0 += PD_THREADS) {
       if (pass == 0 || P.B > PD_THREADS) {
         const int rb = b0 + tid < P.B ? rows_of(b0 + tid) : 0;
-        if (MULTI && b0 + tid < P.B) bad |= min(P.q_start[b0 + tid], P.N) > max(P.q_start[b0 + tid + 1], 0);
+        if (MULTI && b0 + tid < P.B) {
+          const int s = min(P.q_start[b0 + tid], P.N), e = max(P.q_start[b0 + tid + 1], 0);
+          bad |= s > e;
+          some |= (int64_t)(min(e, P.N) - max(s, 0)) * P.G > P.most;
+        }
         n = rb ? weight(decode_span<MULTI>(P, b0 + tid, TILE, rb).n()) * (uint32_t)(C.n_kv_heads * groups(rb)) : 0;
         uint32_t x = n;
 #pragma unroll
@@ -919,9 +925,14 @@ __global__ void __launch_bounds__(PdShape<T, D, NT, MULTI>::THREADS, PdShape<T, 
       }
     }
     if (pass == 0) {
-      if (MULTI && __syncthreads_or(bad)) {              // q_start descends: no work is done
-        if (tid == 0) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
-        return;
+      if (MULTI) {
+        const bool descends = __syncthreads_or(bad);
+        some = __syncthreads_or(some) && !descends;
+        if (blockIdx.x == 0 && tid == 0) *P.some = some;
+        if (descends) {                                  // no work is done
+          if (tid == 0) paged_fail(C.status, ECHO_ERR_INVALID_ARG);
+          return;
+        }
       }
       total = at;
       per = max((total + P.nctas - 1) / P.nctas, whole_items ? 1u : (uint32_t)Sh::MIN_WEIGHT);
@@ -1187,6 +1198,7 @@ __global__ void __launch_bounds__(D) paged_decode_join_kernel(const __grid_const
   __shared__ float red[2][D / 32];
   using Sh = PdShape<T, D, NT, MULTI>;
   constexpr int ROWS = Sh::ROWS;
+  if (MULTI) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c1 = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   const int4 rec = *reinterpret_cast<const int4 *>(P.rec + c1 * 4);
@@ -1262,7 +1274,7 @@ static echo_status_t launch_decode(DecodeParams &P, cudaStream_t st) {
   paged_decode_kernel<T, D, NT, MULTI><<<P.nctas, Sh::THREADS, smem, st>>>(P, kmap, vmap, box);
   ECHO_LAUNCH_OK();
   if (P.whole) return ECHO_OK;
-  ECHO_CUDA_OK(launch_after(paged_decode_join_kernel<T, D, NT, MULTI>, dim3(P.nctas, P.prows), dim3(D), st, P));
+  ECHO_CUDA_OK(launch_after(paged_decode_join_kernel<T, D, NT, MULTI>, dim3(P.nctas, P.prows), dim3(D), 0, st, P));
   return ECHO_OK;
 }
 
@@ -1292,14 +1304,19 @@ static DecodeParams decode_params(const echo_paged_kv_t *cache, const echo_paged
   return P;
 }
 
+static_assert(4 * PD_MULTI_CTAS <= kPgSomeAt, "the records of a call of few tokens lie ahead of the note");
 bool few_tokens_q8(int64_t N, int64_t B, int64_t G, const echo_attn_scores_t *scores) { return !scores->first_tok && N * G <= 32 * B; }
 
 echo_status_t launch_few_tokens_q8(const echo_paged_kv_t *cache, const echo_paged_scales_t *scales, const void *q, int64_t q_stride,
                                    const int32_t *q_start, const int32_t *seq_len, int32_t N, int32_t B, int32_t Hq,
-                                   const echo_attn_scores_t *scores_of, void *out, float *lse, void *workspace, cudaStream_t st) {
+                                   const echo_attn_scores_t *scores_of, int most, void *out, float *lse, void *workspace,
+                                   cudaStream_t st) {
   DecodeParams P = decode_params(cache, scales, q, q_stride, seq_len, B, Hq, scores_of, out, lse, workspace);
   P.q_start = q_start;
   P.N = N;
+  P.most = most;
+  P.some = P.rec + kPgSomeAt;
+  P.po = reinterpret_cast<float *>(P.rec + kPgRecords);
   P.group = fast_div(P.G);
   const bool two = (int64_t)N * P.G <= 16 * (int64_t)B;   // rows of a sequence that two tiles of 8 hold on average
   P.pml = P.po + (size_t)2 * PD_MULTI_CTAS * std::min<int64_t>((int64_t)N * P.G, two ? 16 : 32) * cache->head_dim;

@@ -316,7 +316,7 @@ static echo_status_t launch_simt(const PrefillParams &P, cudaStream_t st) {
   const int grid = std::min(2 * sm_count(), PF_MAX_CTAS);
   paged_prefill_simt_kernel<D><<<grid, PS_THREADS, ps_smem<D>(), st>>>(P);
   ECHO_LAUNCH_OK();
-  ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<float, D>, dim3(grid, (P.prows + 3) / 4), dim3(128), st, P));
+  ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<float, D>, dim3(grid, (P.prows + 3) / 4), dim3(128), 0, st, P));
   return ECHO_OK;
 }
 
@@ -382,6 +382,15 @@ static echo_status_t launch_q8_rows(PrefillParams &P, unsigned char *at, cudaStr
   return ECHO_OK;
 }
 
+// Calls of a few new tokens a sequence on average (few_tokens_q8) over codes.  Up to FEW_ALL_ROWS packed rows go the
+// way of single tokens as they are; of more, sequences of more than FEW_ROWS (the rows that its units hold, and read
+// the cache for) go to the tensor cores, found from q_start on the device: a batch's average tells nothing of its longest
+// sequence.  Measured with 8 KV heads of 128: 255 single tokens of 1K-4K beside 700 tokens of a prompt of 8K 1235 us by the
+// average, 638 so; 2048 rows of one of 1024 sequences (the others empty) 507 and 89 us.  Where no sequence
+// has more the second kernel and its join cost 9 us: 64 x 4 tokens over 2K-6K 201 and 210 us, 256 x 1 over 1K-4K 331 and
+// 340.  Of 1024 rows 31 single tokens beside 97 over 8K take 189 us here and 146 so; 16 x 4 over 17K-20K 208 and 217.
+constexpr int FEW_ROWS = 32, FEW_ALL_ROWS = 1024;
+
 // scales: of a cache in 8 bits, and else NULL.
 static echo_status_t attn_prefill(const echo_paged_kv_t *cache, const echo_paged_scales_t *scales, const void *q,
                                   int64_t q_stride, const int32_t *q_start, const int32_t *seq_len, int32_t N,
@@ -418,8 +427,17 @@ static echo_status_t attn_prefill(const echo_paged_kv_t *cache, const echo_paged
   P.rec = reinterpret_cast<int32_t *>(workspace);
   P.po = reinterpret_cast<float *>(P.rec + 8 * PF_MAX_CTAS);
   P.pml = P.po + (size_t)(bf ? PF_MAX_CTAS : 2 * PF_MAX_CTAS) * P.prows * cache->head_dim;
-  if (scales && few_tokens_q8(N, B, P.G, scores_of))
-    return launch_few_tokens_q8(cache, scales, q, q_stride, q_start, seq_len, N, B, Hq, scores_of, out, lse, workspace, cs);
+  P.above = 0;
+  P.some = nullptr;
+  if (scales && few_tokens_q8(N, B, P.G, scores_of)) {
+    const bool all = (int64_t)N * P.G <= FEW_ALL_ROWS;    // (no sequence has more)
+    const echo_status_t few = launch_few_tokens_q8(cache, scales, q, q_stride, q_start, seq_len, N, B, Hq, scores_of,
+                                                   all ? FEW_ALL_ROWS : FEW_ROWS, out, lse, workspace, cs);
+    if (all || few != ECHO_OK) return few;
+    P.above = FEW_ROWS;
+    P.some = P.rec + kPgSomeAt;
+    return launch_prefill_some(P, cs);
+  }
   if (scales) {
     const size_t base = echo_paged_prefill_workspace_bytes(N, B, Hq, cache->n_kv_heads, cache->head_dim);
     const size_t all = echo_paged_prefill_q8_workspace_bytes(N, B, Hq, cache->n_kv_heads, cache->head_dim, cache->max_pages,

@@ -23,6 +23,9 @@ struct PrefillParams {
   int32_t *rec;                      // [CTAs][8]: the split row tile that ends in the CTA
   int prows;                         // rows of a partial
   int wide;                          // out is 32-byte aligned
+  // SOME: sequences of no more packed rows than `above` are left out, and where *some is 0 there are no others
+  int above;
+  const int32_t *some;
 };
 
 // Rows of sequence b: [s0, s0 + n).
@@ -39,6 +42,7 @@ __device__ __forceinline__ SeqRows seq_rows(const PrefillParams &P, int b) {
 constexpr int PF_MAX_CTAS = 320;     // partial slots: two a CTA
 constexpr int PF_MAX_ROWS = 256;     // packed rows of a row tile: 256 in bf16, 64 in float32
 constexpr int PF_MAX_B = 2048;       // sequences of a call
+static_assert(kPgRecords == 8 * PF_MAX_CTAS && kPgSomeAt >= 8 * (PF_MAX_CTAS / 2), "the bf16 kernel's records end ahead of the note");
 constexpr int PF_ITEM_WEIGHT = 1;    // of a row tile besides its tiles of the cache, in units
 
 // A row tile of one KV head, and its part in a CTA's run of units.
@@ -176,7 +180,7 @@ __device__ __forceinline__ uint32_t plan_scan(PlanShared &S, uint32_t v, uint32_
 }
 // `wt`: shared memory for the weights of PLAN_TILES row tiles, free again when the call ends.
 constexpr int PLAN_TILES = 8192;
-template <int ROWS, int KEYS, int THREADS>
+template <int ROWS, int KEYS, int THREADS, bool SOME = false>
 __device__ __forceinline__ RunPlan prefill_plan(const PrefillParams &P, PlanShared &S, uint32_t *wt) {
   const int tid = threadIdx.x;
   RunPlan pl;
@@ -186,7 +190,8 @@ __device__ __forceinline__ RunPlan prefill_plan(const PrefillParams &P, PlanShar
 #pragma unroll 1
   for (int b0 = 0; b0 < P.B; b0 += THREADS) {
     const int b = b0 + tid;
-    const uint32_t n = b < P.B ? (uint32_t)(((int64_t)seq_rows(P, b).n * P.G + ROWS - 1) / ROWS) : 0;
+    const int64_t rows = b < P.B ? (int64_t)seq_rows(P, b).n * P.G : 0;
+    const uint32_t n = SOME && rows <= P.above ? 0 : (uint32_t)((rows + ROWS - 1) / ROWS);
     bad |= b < P.B && min(P.q_start[b], P.N) > max(P.q_start[b + 1], 0);
     const uint32_t end = base + plan_scan<THREADS>(S, n, sum);
     if (b < P.B) S.tiles[b] = (int)(end - n);
@@ -315,9 +320,10 @@ __device__ __forceinline__ void join_record(const PrefillParams &P, int c0, int 
 // Joins the partials of the row tile that ends in CTA blockIdx.x, in the order of their units:
 // slot 1 of its first CTA, then slot 0 of the following ones.  A warp takes a row: the maximum
 // of all first, so that the weighted sums are independent loads.
-template <typename T, int D>
+template <typename T, int D, bool SOME = false>
 __global__ void __launch_bounds__(128) paged_prefill_join_kernel(const __grid_constant__ PrefillParams P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (SOME && *P.some == 0) return;
   const int c1 = blockIdx.x;
   const int4 ra = *reinterpret_cast<const int4 *>(P.rec + c1 * 8), rb = *reinterpret_cast<const int4 *>(P.rec + c1 * 8 + 4);
   if (ra.x == 0) return;
@@ -367,6 +373,7 @@ __global__ void __launch_bounds__(128) paged_prefill_join_kernel(const __grid_co
 
 echo_status_t launch_prefill_tc(PrefillParams &P, cudaStream_t st);   // bf16
 echo_status_t launch_prefill_q8(PrefillParams &P, cudaStream_t st);   // e4m3 codes, bf16 queries
+echo_status_t launch_prefill_some(PrefillParams &P, cudaStream_t st); // that, of sequences of more than P.above packed rows
 echo_status_t launch_prefill_rows(PrefillParams &P, cudaStream_t st); // rows that were codes
 
 }  // namespace echo

@@ -290,7 +290,8 @@ static __device__ __noinline__ float pt_query(uint32_t tile, int r) {
   return exp2i(-up);
 }
 
-template <int D, int MOD, bool ALT, int IN>
+// SOME: beside a call of a few tokens a sequence.
+template <int D, int MOD, bool ALT, int IN, bool SOME>
 __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const __grid_constant__ PrefillParams P,
                                                                         const __grid_constant__ CUtensorMap kmap,
                                                                         const __grid_constant__ CUtensorMap vmap,
@@ -314,6 +315,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const echo_paged_kv_t &C = P.C;
   const int G = P.G;
+  if (SOME) {                                             // (launched under the tail of the few tokens' join)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (*P.some == 0) return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
     if (qbox) tma_prefetch_desc(&qmap);
   }
 
-  const RunPlan pl = prefill_plan<ROWS, PT_KEYS, PT_THREADS>(P, S.plan, reinterpret_cast<uint32_t *>(R));
+  const RunPlan pl = prefill_plan<ROWS, PT_KEYS, PT_THREADS, SOME>(P, S.plan, reinterpret_cast<uint32_t *>(R));
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
@@ -1112,12 +1117,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) paged_prefill_tc_kernel(const _
   if (warp == 11) tmem_dealloc(tmem, 512);
 }
 
-template <int D, int MOD, bool ALT, int IN>
+template <int D, int MOD, bool ALT, int IN, bool SOME = false>
 static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
   constexpr bool Q8 = IN == PT_CODES;
   constexpr size_t smem = pt_smem<D, ALT, IN>();
   static_assert(smem <= 227 * 1024, "fits an SM");
-  ECHO_CUDA_OK((allow_smem<paged_prefill_tc_kernel<D, MOD, ALT, IN>>(smem)));
+  ECHO_CUDA_OK((allow_smem<paged_prefill_tc_kernel<D, MOD, ALT, IN, SOME>>(smem)));
   int box = std::min(P.C.page_tokens & -P.C.page_tokens, PT_KEYS);
   int qbox = !Q8 && 128 % P.G == 0 ? 128 / P.G : 0;
   CUtensorMap kmap = {}, vmap = {}, qmap = {};
@@ -1137,9 +1142,14 @@ static echo_status_t launch_tc(PrefillParams &P, cudaStream_t st) {
     if (qbox && !pg_map(&qmap, P.q, ECHO_BF16, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B)) qbox = 0;
   }
   const int grid = std::min(sm_count(), PF_MAX_CTAS / 2);
-  paged_prefill_tc_kernel<D, MOD, ALT, IN><<<grid, PT_THREADS, smem, st>>>(P, kmap, vmap, qmap, box, qbox);
-  ECHO_LAUNCH_OK();
-  ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<__nv_bfloat16, D>, dim3(grid, (P.prows + 3) / 4), dim3(128), st, P));
+  if (SOME) {
+    ECHO_CUDA_OK(launch_after(paged_prefill_tc_kernel<D, MOD, ALT, IN, SOME>, dim3(grid), dim3(PT_THREADS), smem, st, P, kmap, vmap, qmap, box, qbox));
+  } else {
+    paged_prefill_tc_kernel<D, MOD, ALT, IN, SOME><<<grid, PT_THREADS, smem, st>>>(P, kmap, vmap, qmap, box, qbox);
+    ECHO_LAUNCH_OK();
+  }
+  // (SOME: blocks that find nothing to do are launched as well, and are fewer)
+  ECHO_CUDA_OK(launch_after(paged_prefill_join_kernel<__nv_bfloat16, D, SOME>, dim3(grid, SOME ? (P.prows + 15) / 16 : (P.prows + 3) / 4), dim3(128), 0, st, P));
   return ECHO_OK;
 }
 
