@@ -466,10 +466,6 @@ _SCALES = struct.Struct("@PPqqq")
 _NORM = struct.Struct("@PPf4x")
 _BF, _FL, _INT = torch.bfloat16, torch.float32, torch.int32
 _F8, _E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
-try:                        # torch.empty on the current device without its parsing of arguments: 3 us less a call of three
-    from torch._C._dynamo.guards import _empty_strided_cuda as _empty_cuda
-except ImportError:
-    _empty_cuda = None
 
 
 def _bad(where: str, what: str):
@@ -572,13 +568,7 @@ def _empty(shape, dt, dev, stream, kept: bool = True):
     given stream does not wait for that.  Recorded on the current stream, where a kept one is
     likely used."""
     if stream is None:
-        if _empty_cuda is None:
-            return torch.empty(shape, dtype=dt, device=dev)
-        shape, strides, n = tuple(shape), [], 1            # (on the current device, which the caches' is)
-        for k in reversed(shape):
-            strides.append(n)
-            n *= k
-        return _empty_cuda(shape, tuple(strides[::-1]), dt)
+        return torch.empty(shape, dtype=dt, device=dev)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dt, device=dev)
     if kept:
