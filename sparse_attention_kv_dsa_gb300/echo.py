@@ -465,7 +465,7 @@ _SCORES = struct.Struct("@ffPiPP")
 _SCALES = struct.Struct("@PPqqq")
 _NORM = struct.Struct("@PPf4x")
 _BF, _FL, _INT = torch.bfloat16, torch.float32, torch.int32
-_F8, _E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_F8, _E8 = torch.float8_e4m3fn, getattr(torch, "float8_e8m0fnu", None)
 
 
 def _bad(where: str, what: str):
