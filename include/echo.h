@@ -737,9 +737,9 @@ echo_status_t echo_paged_attn_prefill(const echo_paged_kv_t *cache, const void *
  * e, the smallest in -15 .. 7 with max|x| <= 448 * 2^e (7 if there is none):
  *   code = e4m3(x * 2^-e), to nearest even, saturating;   value = code * 2^e.
  * A power of two costs an e4m3 code no precision: a row's values are off by 2^-4 of themselves, or by
- * 2^-10 * 2^e (2^-18 of the row's largest value while e > -15) at most, and x * 2^-e, code * 2^e are exact.
- * Every code * 2^e is a float16 number: values past 57344 saturate, the least step is 2^-24, and the
- * tensor cores take them as they are.
+ * 2^-10 * 2^e (2^-17 of the row's largest value while e > -15) at most, and x * 2^-e, code * 2^e are exact.
+ * Every code * 2^e is a float16 number: values past 57344 saturate (status does not tell), the least step is
+ * 2^-24, and the tensor cores take them as they are.
  *
  * echo_paged_kv_t describes the codes: dtype ECHO_E4M3, strides in codes, still multiples of 16
  * bytes.  The exponent of KV head h of row i of page p is the byte e + 127 (e8m0, the number 2^e)
@@ -793,12 +793,15 @@ echo_status_t echo_paged_append_q8(const echo_paged_kv_t *cache, const echo_page
  * echo_paged_prefill_q8_workspace_bytes it writes the tokens that a sequence's rows see (from the smallest lower end of
  * them on, and by a prefix) out in 16 bits first, exactly, where packed rows are many: 1024 (token, query head of a KV
  * head) pairs a sequence or more on average over N and B, and a page table whose max_pages * page_tokens bound
- * what could be written by 1 GiB (the workspace's size goes by them).  Otherwise the two sizes are the same.  Where N
- * packed rows are 32 a sequence or fewer on average and first_tok is NULL, sequences with 32 at most take
- * echo_paged_attn_decode_q8's way, in calls of up to 1024 rows those with more too.
- * The codes are not rounded again.  Scores are float32 sums of products of codes and a query, which is scaled
- * by a power of two to float16 (exact where it is above 2^-31 of its head's largest value); weights are
- * rounded to float16, and those below 2^-31 of a row's largest may be lost.  Codes and exponents of tokens that no row sees may be anything.
+ * what could be written by 1 GiB (the workspace's size goes by them).  Otherwise the two sizes are the same.  Where
+ * the packed rows are 32 a sequence or fewer on average and first_tok is NULL, sequences with 32 at most go the way of
+ * echo_paged_attn_decode_q8 (in calls of up to 1024 packed rows those with more too), the others that of chunks.
+ * The codes are not rounded again.  Scores are float32 sums of products of the keys and a query: as it is on rows
+ * written out, and else scaled by a power of two to float16, exactly where it is above 2^-30 of its head's largest value
+ * (of heads below 2^-87: above 2^-117).  Weights are rounded to float16, by 2^-11 of themselves at most, or by 2^-31 of
+ * the row's largest; one token at a time, and on the way of a few rows, it is their products with the values'
+ * powers of two that are, by 2^-11, or by 2^-35 of the row's largest such product.  Codes and exponents of tokens
+ * that no row sees may be anything.
  */
 echo_status_t echo_paged_attn_decode_q8(const echo_paged_kv_t *cache, const echo_paged_scales_t *scales,
                                         const void *q, int64_t q_stride, const int32_t *seq_len, int32_t B,

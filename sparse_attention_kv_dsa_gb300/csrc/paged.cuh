@@ -94,7 +94,8 @@ __device__ __forceinline__ int q8_row_exp(float amax) {
   return min(max(e, kQ8MinExp), kQ8MaxExp);
 }
 // The power of two that brings a query's largest value into [2^13, 2^14), as float16 holds it: products
-// with codes stay below 2^23, and what is 2^-31 of the largest value or more keeps its bits.
+// with codes stay below 2^23, and what is 2^-30 of the largest value or more keeps its bits (eight of them, down to
+// float16's step of 2^-24).  Heads below 2^-87 stay smaller.
 __device__ __forceinline__ int q8_query_exp(float amax) {
   const int e = 13 + 127 - (int)(__float_as_uint(amax) >> 23);
   return amax == 0.f ? 0 : min(max(e, -114), 100);
