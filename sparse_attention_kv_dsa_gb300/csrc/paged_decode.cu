@@ -48,7 +48,7 @@
 // 333 us), 64 tokens a warp at d = 64 (96 sequences 86 us).
 //
 // A few new tokens a sequence over codes (MULTI; up to 32 rows, (new token, query head of the group) pairs, a
-// sequence on average, no document starts): the same split and loop with up to 32 rows to a unit,
+// sequence on average, no document starts; sequences with more rows than `most` are another kernel's): the same split and loop with up to 32 rows to a unit,
 // each with its own end.  The tensor-core kernel of the many-token call spends its single warps' turns
 // there (16 sequences of 17K-20K with 4 new tokens each 287 us on 128-row tiles).  Here 205 us, 3.1 TB/s: eight
 // warps of 255 registers an SM, latency (1.8 stalled warps an issue wait for the instruction before, issue

@@ -54,7 +54,8 @@
 // 64 heads of 128 over 8, 128 tokens over 32K 166 us (128 with the cache in bf16), 512 over 32K 557 us (385).
 // Rows that many row tiles read are therefore written out in 16 bits first (paged_prefill.cu; PT_WRITTEN), and a few rows a sequence go the
 // way of single tokens (paged_decode.cu); what is left for it are 33 to 1023 rows a sequence on
-// average, documents, and page tables too large to write out.  Code that is not small costs every warp
+// average, few ones with documents, page tables too large to write out, and (SOME) sequences of more than 32 rows
+// among many of few.  Code that is not small costs every warp
 // of the kernel (missing instructions: 1.9 stalled warps an issue against 0.5 in bf16).
 
 #pragma once

@@ -48,7 +48,7 @@ def test_chunks_beside_single_tokens_modifiers(kw, d):
     _prefill(*MIXED, 16, 8, 1, d, seed=3, **kw)
 
 
-@pytest.mark.parametrize("new", [[4] * 32, [4] * 30 + [3, 5], [4] * 33, [4] * 36 + [3, 5], [0] * 39 + [129], [0] * 40 + [128], [33] + [1] * 140])
+@pytest.mark.parametrize("new", [[4] * 32, [4] * 30 + [3, 5], [4] * 33, [4] * 36 + [3, 5], [0] * 39 + [129], [0] * 40 + [128], [33] + [1] * 140, [1] * 699 + [60, 0, 1]])
 def test_borders_of_the_kernels_rows(new):
     """32 and 33 packed rows of a sequence and more, 1024 of a call and more, at 8 heads to a KV head."""
     N = max(sum(new), 100)
