@@ -338,7 +338,9 @@ extern "C" size_t echo_paged_prefill_workspace_bytes(int32_t N, int32_t B, int32
 // Where a cache in 8 bits is written out in 16 bits first.  Turning a tile's codes costs the tensor-core kernel
 // some 0.7 us each time that a row tile reads it; writing them out and reading them back, 3 bytes a
 // value of HBM, is 2.5 us a tile, once.  A prompt of 8192, 64 heads over 8: 1430 us on the codes, 932 written
-// out first; 512 tokens over 32K, capped: 500 and 448 (424 since).
+// out first; 512 tokens over 32K, capped: 500 and 448 (424 since).  The rule goes by averages, and mixtures bear it: 4096
+// tokens beside 30 single ones of 1K 481 on the codes, 351 written out, of 8K 708 and 751; 1024 beside 7 of 32K 375 both.
+// A GiB holds 256K tokens of 8 heads of 128: some 0.3 ms of HBM at most where few rows read them.
 static bool q8_rows_first(int64_t N, int64_t B, int64_t G, int64_t bytes) {
   return N * G >= 4 * PF_MAX_ROWS * B && bytes <= (1ll << 30);
 }
